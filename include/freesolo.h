@@ -59,7 +59,11 @@ typedef enum {
     FS_ERR_KERNEL_CHECK = 6   /* a kernel's internal consistency check failed (device flag) */
 } fs_status;
 
-typedef enum { FS_BF16 = 0, FS_F32 = 1 } fs_dtype;
+typedef enum {
+    FS_BF16 = 0,
+    FS_F32 = 1,
+    FS_F16 = 2   /* rotary positions and the paged cache only */
+} fs_dtype;
 
 #define FS_MAX_HEADS 256
 
@@ -310,6 +314,148 @@ fs_status fs_select_topk_tree(const fs_params *p, const void *Q, const void *for
 fs_status fs_forward_tree(const fs_params *p, const void *Q, const void *K, const void *V, const float *tau,
                           int beam, float c_explore, int32_t *idx, void *O, void *ws, size_t ws_bytes,
                           void *forest, size_t forest_bytes, void *stream);
+
+/* ---- rotary positions ----
+ * The pairs of the first r of a row's d elements turn by pos * theta_m:
+ *     (y_1, y_2) = mscale (x_1 cos - x_2 sin, x_1 sin + x_2 cos),
+ * the pairs being (2m, 2m+1) (FS_ROPE_INTERLEAVED, as eq. (3) is read above) or (m, m + r/2)
+ * (FS_ROPE_HALF); the other d - r elements are copied.  theta_m = base^(-2m/r), for contexts
+ * longer than the trained one by `factor` >= 1 scaled as
+ *     FS_ROPE_LINEAR    theta_m / factor
+ *     FS_ROPE_NTK       base factor^(r/(r-2)) in the place of base
+ *     FS_ROPE_BY_PARTS  theta_m ((1-g)/factor + g), g = clamp((n_m - slow)/(fast - slow), 0, 1),
+ *                       n_m = orig_len theta_m / 2 pi the turns of pair m over the trained context.
+ * Angles are right to 2^-32 turns at every 32-bit position; products and sums are fp32, each
+ * output is rounded once. */
+#define FS_ROPE_MAX_R 256
+typedef enum { FS_ROPE_INTERLEAVED = 0, FS_ROPE_HALF = 1 } fs_rope_layout;
+typedef enum { FS_ROPE_NONE = 0, FS_ROPE_LINEAR = 1, FS_ROPE_NTK = 2, FS_ROPE_BY_PARTS = 3 } fs_rope_scaling;
+
+/* A rotation, made once by fs_rotary_init (host memory, no device state; copied by each call). */
+typedef struct {
+    int r;                                /* rotated elements: even, 2 <= r <= FS_ROPE_MAX_R */
+    fs_rope_layout layout;
+    float mscale;                         /* multiplies the rotated elements (1: a pure rotation) */
+    uint64_t turns[FS_ROPE_MAX_R / 2];    /* theta_m / 2 pi in units of 2^-64 */
+} fs_rotary;
+
+/* Fills `out`.  base >= 1.  factor is read unless scaling is FS_ROPE_NONE; orig_len > 0 and
+ * 0 <= slow < fast by FS_ROPE_BY_PARTS alone. */
+fs_status fs_rotary_init(int r, fs_rope_layout layout, double base, fs_rope_scaling scaling, double factor,
+                         double orig_len, double slow, double fast, double mscale, fs_rotary *out);
+
+typedef struct {
+    int B, N;                 /* rows of positions; T = B N tokens */
+    int H, Hk;                /* heads of the first tensor (Q) and of the second (K; 0: none) */
+    int d;                    /* elements of a row, r <= d <= FS_ROPE_MAX_R */
+    long long q[3], qo[3];    /* strides over (b, h, n) in elements; a row's elements are contiguous */
+    long long k[3], ko[3];
+    fs_dtype dtype;           /* FS_BF16, FS_F16 or FS_F32 */
+} fs_rope_params;
+
+/* Rotates Q [B,H,N,d] into Qo and K [B,Hk,N,d] into Ko (any strides; outputs whose strides fold
+ * elements together are FS_ERR_INVALID_ARG).  An output may be its own input with the same
+ * strides, but may not overlap it otherwise.  pos: device int32, token (b, n) at
+ * pos[b pos_stride + n] (pos_stride 0: shared by the rows); NULL: position pos0 + n.  Rows that
+ * start on 16-byte boundaries and whose parts are whole 16-byte vectors are moved in vectors,
+ * others element by element.  B, N or H + Hk of 0 does nothing. */
+fs_status fs_rope(const fs_rope_params *p, const fs_rotary *rot, const void *Q, void *Qo, const void *K, void *Ko,
+                  const int32_t *pos, long long pos_stride, long long pos0, void *stream);
+
+/* Its gradient: dQ = mscale R(-pos) dQo, the same for K; q / k are the strides of dQo / dKo and
+ * qo / ko those of dQ / dK.  Everything else as for fs_rope. */
+fs_status fs_rope_backward(const fs_rope_params *p, const fs_rotary *rot, const void *dQo, void *dQ, const void *dKo,
+                           void *dK, const int32_t *pos, long long pos_stride, long long pos0, void *stream);
+
+/* ---- paged key-value cache: many sequences in one pool of pages ----
+ * The pools Kp, Vp hold num_pages pages of page_size tokens for each of Hkv heads, element
+ * (page, head, slot, e) at page page_stride + head head_stride + slot token_stride + e (both
+ * pools alike; [num_pages, Hkv, page_size, d] and [num_pages, page_size, Hkv, d] are the usual
+ * orders).  Sequence b holds lens[b] tokens: token t in slot t % page_size of page
+ * table[b][t / page_size].  table is int32 [B, max_pages], lens int32 [B], refs int32
+ * [num_pages]: how many table rows list the page (0: the page is free).  All are device arrays
+ * that the caller owns; a new cache has table = -1, lens = 0, refs = 0.
+ *
+ * Supported: d = 64, 128 or 256; H a multiple of Hkv; any page_size >= 1 with
+ * max_pages page_size < 2^30; num_pages <= 2,000,000; strides that are multiples of 16 bytes and keep the elements of a
+ * pool apart (pools of any size: offsets are 64-bit); dtype bf16, f16 or f32.
+ *
+ * ws: fs_paged_workspace_size bytes of device workspace, zero-filled once; its first bytes hold
+ * the device error flag read by fs_sync_status.  Calls that share a workspace must be ordered
+ * (one stream, or graphs that do not overlap); between calls it carries nothing but the flag.
+ * A table entry outside [0, num_pages) that a call needs, a length outside
+ * [0, max_pages page_size] and the like set the flag (FS_ERR_KERNEL_CHECK); no call reads or
+ * writes outside the pools for them. */
+typedef struct {
+    int B;                    /* sequences: rows of table and lens */
+    int H, Hkv, d;            /* query heads, key-value heads, head dim */
+    int page_size, num_pages, max_pages;
+    long long page_stride, head_stride, token_stride;   /* elements */
+    fs_dtype dtype;
+} fs_paged_params;
+
+fs_status fs_paged_workspace_size(const fs_paged_params *p, size_t *bytes);
+
+/* Writes the newest tokens of the sequences into their pages.  K_new, V_new are [T, Hkv, d], rows
+ * k_stride / v_stride elements apart, heads d apart.  Sequence b's tokens are the rows
+ * cu[b] .. cu[b+1]-1 (cu: device int32 [B+1], not decreasing from cu[0] = 0) and take its last
+ * positions, lens[b] - n .. lens[b] - 1: lens already counts them (fs_pages_reserve).  cu NULL:
+ * one row each, T = B, and a sequence with lens[b] = 0 is skipped.  Rows from cu[B] on are
+ * padding and are not read; their Qo rows are left as they were.
+ * rot (NULL: none): the keys are rotated by their positions as they are written, and so are the
+ * query rows Q [T, H, d] into Qo (Q NULL: none; Q == Qo with the same stride: in place).  The
+ * rows of a token that has no place (flagged) are skipped.  Rows start on 16-byte boundaries. */
+fs_status fs_paged_append(const fs_paged_params *p, const fs_rotary *rot, int T, const void *Q, long long q_stride,
+                          void *Qo, long long qo_stride, const void *K_new, long long k_stride, const void *V_new,
+                          long long v_stride, const int32_t *cu, void *Kp, void *Vp, const int32_t *table,
+                          const int32_t *lens, void *ws, size_t ws_bytes, void *stream);
+
+/* Attention of one new token per sequence over its pages: query row b (position lens[b] - 1)
+ * sees the keys j in [max(0, lens[b] - 1 - window), lens[b] - 1] (window < 0: all),
+ *     O[b,h] = sum_j softmax_j(scale q.k_j) v_j  with the keys of head h / (H / Hkv),
+ *     lse[b,h] = log sum_j exp(scale q.k_j)   (float32, NULL: not wanted).
+ * Q, O: [B, H, d], rows b q_stride / o_stride elements apart, heads d apart.  With keys written
+ * rotated and window = w this is o^sr of eq. (3).  lens[b] = 0: O = 0 and lse = -inf.
+ * bf16, f16: products on the tensor cores, fp32 softmax and sums, the probabilities rounded to
+ * the type for the product with V; f32: fp32 throughout.  What pages hold behind the last token
+ * is never used, NaN included. */
+fs_status fs_paged_attend(const fs_paged_params *p, const void *Q, long long q_stride, const void *Kp, const void *Vp,
+                          const int32_t *table, const int32_t *lens, int window, float scale, void *O,
+                          long long o_stride, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Room for n_new[b] >= 0 more tokens of every sequence (device int32 [B]): takes the lowest free
+ * pages, in the order of the sequences and of their positions, writes them into table, sets
+ * their refs to 1 and adds n_new to lens.  All or nothing: if there are too few free pages or a
+ * sequence would outgrow max_pages, nothing changes and the flag is set.  A sequence whose last
+ * page is part filled must be that page's only holder (fs_pages_fork sees to it). */
+fs_status fs_pages_reserve(const fs_paged_params *p, const int32_t *n_new, int32_t *refs, int32_t *table,
+                           int32_t *lens, void *ws, size_t ws_bytes, void *stream);
+
+/* Page dst[i] becomes a copy of page src[i] in both pools, i < n (device int32).  The dst pages
+ * are distinct and none of them is a src. */
+fs_status fs_pages_copy(const fs_paged_params *p, void *Kp, void *Vp, const int32_t *src, const int32_t *dst, int n,
+                        void *ws, size_t ws_bytes, void *stream);
+
+/* Sequence dst[i] (empty) becomes a branch of sequence src[i], i < n (device int32; a src may
+ * occur often, the dst are distinct and none is a src): whole pages are shared (their refs count
+ * it), a part-filled last page is copied, as far as it is filled, into the lowest free page, in
+ * the order of i.  All or nothing, as fs_pages_reserve. */
+fs_status fs_pages_fork(const fs_paged_params *p, void *Kp, void *Vp, int32_t *refs, int32_t *table, int32_t *lens,
+                        const int32_t *src, const int32_t *dst, int n, void *ws, size_t ws_bytes, void *stream);
+
+/* Sequences rows[i], i < n (device int32), give their pages back: refs count down, the entries
+ * become -1 and lens 0.  An empty sequence, or one listed twice, is nothing more to free. */
+fs_status fs_pages_free(const fs_paged_params *p, int32_t *refs, int32_t *table, int32_t *lens, const int32_t *rows,
+                        int n, void *ws, size_t ws_bytes, void *stream);
+
+/* Packs the L pages in use into the pages 0 .. L-1: the i-th used page from L on moves to the
+ * i-th free page below L.  refs_out [num_pages] and table_out [B, max_pages] are the packed
+ * cache's (they may be refs and table themselves; otherwise those stay as they are); live (NULL:
+ * not wanted) receives L.  Entries below 0 and entries of free pages are copied as they are.
+ * Pages that are free afterwards keep their bytes. */
+fs_status fs_pages_compact(const fs_paged_params *p, void *Kp, void *Vp, const int32_t *refs, const int32_t *table,
+                           int32_t *refs_out, int32_t *table_out, int32_t *live, void *ws, size_t ws_bytes,
+                           void *stream);
 
 /* ---- diagnostics (no counterpart in the method: measurement support) ----
  * fs_launch_count: kernels this library has launched since load (all calls, streams).

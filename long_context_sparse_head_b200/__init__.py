@@ -9,7 +9,10 @@ long_context_sparse_head_b200.build).
 The entry points mirror the C names: `workspace_size`, `cell_summaries`, `select_topk`,
 `forward`, `host_scratch_size`, `forward_host`, `sync_status`, `status_string`, and the
 FS-L streaming cache `cache_bytes`, `cache_reset`, `cache_append`, `cache_attend`,
-`cache_status`.
+`cache_status`.  Serving many sequences at once: `Rotary`, `rope`, `rope_backward` (rotary
+positions), `PagedParams`, `paged_append`, `paged_attend` (a cache in pages and attention of
+one new token per sequence over it) and `pages_reserve`, `pages_copy`, `pages_fork`,
+`pages_free`, `pages_compact` (its pages).
 """
 import ctypes
 import os
@@ -19,7 +22,8 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfreesolo.so")
 
-FS_BF16, FS_F32 = 0, 1
+FS_BF16, FS_F32, FS_F16 = 0, 1, 2
+FS_ROPE_MAX_R = 256
 STATUS = {0: "FS_OK", 1: "FS_ERR_INVALID_ARG", 2: "FS_ERR_UNSUPPORTED", 3: "FS_ERR_WORKSPACE",
           4: "FS_ERR_CUDA", 5: "FS_ERR_TIMEOUT", 6: "FS_ERR_KERNEL_CHECK"}
 EXPORTS = ("fs_workspace_size", "fs_cell_summaries", "fs_select_topk", "fs_forward",
@@ -28,7 +32,10 @@ EXPORTS = ("fs_workspace_size", "fs_cell_summaries", "fs_select_topk", "fs_forwa
            "fs_select_topk_noalloc", "fs_cache_bytes", "fs_cache_reset", "fs_cache_append",
            "fs_cache_attend", "fs_cache_status", "fs_select_topk_rerank", "fs_forward_rerank",
            "fs_backward_workspace_size", "fs_backward", "fs_forest_bytes", "fs_forest_build",
-           "fs_select_topk_tree", "fs_forward_tree", "fs_forest_append", "fs_selftest_timeout")
+           "fs_select_topk_tree", "fs_forward_tree", "fs_forest_append", "fs_selftest_timeout",
+           "fs_rotary_init", "fs_rope", "fs_rope_backward", "fs_paged_workspace_size", "fs_paged_append",
+           "fs_paged_attend", "fs_pages_reserve", "fs_pages_copy", "fs_pages_fork", "fs_pages_free",
+           "fs_pages_compact")
 
 
 class FsError(RuntimeError):
@@ -49,6 +56,22 @@ class FsParams(ctypes.Structure):
         ("rms_eps", ctypes.c_float),
         ("dtype", ctypes.c_int),
     ]
+
+
+class FsRotary(ctypes.Structure):
+    _fields_ = [("r", ctypes.c_int), ("layout", ctypes.c_int), ("mscale", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * (FS_ROPE_MAX_R // 2))]
+
+
+class FsRopeParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "N", "H", "Hk", "d")] +
+                [(n, ctypes.c_longlong * 3) for n in ("q", "qo", "k", "ko")] + [("dtype", ctypes.c_int)])
+
+
+class FsPagedParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "H", "Hkv", "d", "page_size", "num_pages", "max_pages")] +
+                [(n, ctypes.c_longlong) for n in ("page_stride", "head_stride", "token_stride")] +
+                [("dtype", ctypes.c_int)])
 
 
 _lib = None
@@ -98,6 +121,20 @@ def load():
         L.fs_forward_tree.argtypes = [P, vp, vp, vp, fp, ctypes.c_int, ctypes.c_float, vp, vp, vp, sz, vp,
                                       sz, vp]
         L.fs_selftest_timeout.argtypes = [vp, vp]
+        i32, i64, f32, f64 = ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_double
+        PP = ctypes.POINTER(FsPagedParams)
+        L.fs_rotary_init.argtypes = [i32, i32, f64, i32, f64, f64, f64, f64, f64, ctypes.POINTER(FsRotary)]
+        L.fs_rope.argtypes = [ctypes.POINTER(FsRopeParams), ctypes.POINTER(FsRotary), vp, vp, vp, vp, vp, i64, i64, vp]
+        L.fs_rope_backward.argtypes = L.fs_rope.argtypes
+        L.fs_paged_workspace_size.argtypes = [PP, ctypes.POINTER(sz)]
+        L.fs_paged_append.argtypes = [PP, ctypes.POINTER(FsRotary), i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
+                                      vp, vp, vp, vp, sz, vp]
+        L.fs_paged_attend.argtypes = [PP, vp, i64, vp, vp, vp, vp, i32, f32, vp, i64, vp, vp, sz, vp]
+        L.fs_pages_reserve.argtypes = [PP, vp, vp, vp, vp, vp, sz, vp]
+        L.fs_pages_copy.argtypes = [PP, vp, vp, vp, vp, i32, vp, sz, vp]
+        L.fs_pages_fork.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+        L.fs_pages_free.argtypes = [PP, vp, vp, vp, vp, i32, vp, sz, vp]
+        L.fs_pages_compact.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         for name in EXPORTS:
             if name not in ("fs_status_string", "fs_launch_count", "fs_kernel_name"):
                 getattr(L, name).restype = ctypes.c_int
@@ -339,6 +376,287 @@ def cache_status(cache, stream=None):
     _check(load().fs_cache_status(_ptr(cache), _stream(stream)), "fs_cache_status")
 
 
+# ---- serving: what the calls below share ---------------------------------------------
+def _need(ok, where, what):
+    if not ok:
+        raise FsError(1, "%s: %s" % (where, what))
+
+
+_DTYPES = {}
+
+
+def _dtype(t, where):
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: FS_BF16, torch.float32: FS_F32, torch.float16: FS_F16})
+    code = _DTYPES.get(t.dtype)
+    _need(code is not None, where, "tensors are bf16, f16 or f32")
+    return code
+
+
+class _On:
+    """The device of a call's tensors made current, and its stream (the current one unless given)."""
+
+    def __init__(self, where, stream, *tensors):
+        import torch
+        self.dev = dev = tensors[0].device
+        _need(dev.type == "cuda", where, "tensors are on a CUDA device")
+        for t in tensors:
+            _need(t.device == dev, where, "all tensors are on one device")
+        self.stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+        self.was = torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.was != self.dev.index:
+            import torch
+            torch.cuda.set_device(self.dev)
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.was != self.dev.index:
+            import torch
+            torch.cuda.set_device(self.was)
+
+
+# ---- rotary positions ----------------------------------------------------------------
+class Rotary:
+    """A rotation of the first r elements of a row: layout "interleaved" (pairs 2m, 2m+1) or
+    "half" (pairs m, m + r/2); frequencies base^(-2m/r), for contexts longer by `factor` scaled
+    "linear", "ntk" or "by_parts" (orig_len, slow, fast); mscale multiplies what is rotated."""
+    LAYOUTS = {"interleaved": 0, "half": 1}
+    SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+    def __init__(self, r, layout="interleaved", base=10000.0, scaling="none", factor=1.0, orig_len=0.0, slow=1.0,
+                 fast=32.0, mscale=1.0):
+        _need(layout in self.LAYOUTS and scaling in self.SCALINGS, "Rotary", "layout or scaling unknown")
+        self.c = FsRotary()
+        _check(load().fs_rotary_init(int(r), self.LAYOUTS[layout], base, self.SCALINGS[scaling], factor, orig_len,
+                                     slow, fast, mscale, ctypes.byref(self.c)), "fs_rotary_init")
+        self.r, self.layout = int(r), layout
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def _rope(fn, where, rotary, Q, Qo, K, Ko, positions, pos0, stream):
+    _need((K is None) == (Ko is None), where, "K and its output come together")
+    _need(Q.dim() == 4 and Q.shape == Qo.shape and Qo.dtype == Q.dtype, where, "Q and its output are [B,H,N,d]")
+    B, H, N, d = Q.shape
+    c = FsRopeParams()
+    c.B, c.N, c.H, c.d, c.dtype = B, N, H, d, _dtype(Q, where)
+    ts = [Q, Qo]
+    for t, s in ((Q, c.q), (Qo, c.qo)) if K is None else ((Q, c.q), (Qo, c.qo), (K, c.k), (Ko, c.ko)):
+        st = t.stride()
+        _need(d == 1 or st[3] == 1, where, "a row's elements are contiguous")
+        s[:] = st[:3]
+    if K is not None:
+        _need(K.dim() == 4 and K.shape == Ko.shape and K.dtype == Ko.dtype == Q.dtype and K.shape[0] == B and
+              K.shape[2] == N and K.shape[3] == d, where, "K and its output are [B,Hk,N,d] of Q's type")
+        c.Hk = K.shape[1]
+        ts += [K, Ko]
+    ps = 0
+    if positions is not None:
+        _need(positions.dtype.itemsize == 4 and not positions.is_floating_point(), where, "positions are int32")
+        _need(tuple(positions.shape) in ((N,), (B, N)) and (N <= 1 or positions.stride(-1) == 1), where,
+              "positions are [N] or [B,N], a row contiguous")
+        ps = positions.stride(0) if positions.dim() == 2 else 0
+        ts.append(positions)
+    with _On(where, stream, *ts) as st:
+        _check(fn(ctypes.byref(c), rotary.ref(), Q.data_ptr(), Qo.data_ptr(), _ptr(K), _ptr(Ko), _ptr(positions), ps,
+                  int(pos0), st), where)
+
+
+def rope(rotary, Q, Qo, K=None, Ko=None, positions=None, pos0=0, stream=None):
+    """Rotates Q [B,H,N,d] into Qo and K [B,Hk,N,d] into Ko (views of any strides with contiguous
+    rows; an output may be its input): token (b, n) by positions[b, n] or [n] (int32), or pos0 + n."""
+    _rope(load().fs_rope, "fs_rope", rotary, Q, Qo, K, Ko, positions, pos0, stream)
+
+
+def rope_backward(rotary, dQo, dQ, dKo=None, dK=None, positions=None, pos0=0, stream=None):
+    """Gradients of rope: dQ, dK from the gradients dQo, dKo of its outputs."""
+    _rope(load().fs_rope_backward, "fs_rope_backward", rotary, dQo, dQ, dKo, dK, positions, pos0, stream)
+
+
+# ---- paged key-value cache -----------------------------------------------------------
+class PagedParams:
+    """fs_paged_params: B sequences over a pool of num_pages pages of page_size tokens; H query
+    and Hkv key-value heads of dim d.  The pools are tensors [num_pages, Hkv, page_size, d] with
+    these strides (elements): layout "heads_first" (contiguous) or "tokens_first" (a view of
+    [num_pages, page_size, Hkv, d]), or `strides` of one's own (page, head, token)."""
+
+    def __init__(self, *, B, H, Hkv, page_size, num_pages, max_pages, d=64, dtype="bf16", layout="heads_first",
+                 strides=None):
+        _need(dtype in ("bf16", "f32", "f16") and layout in ("heads_first", "tokens_first"), "PagedParams",
+              "dtype or layout unknown")
+        if strides is None:
+            page = Hkv * page_size * d
+            strides = (page, page_size * d, d) if layout == "heads_first" else (page, d, Hkv * d)
+        self.B, self.H, self.Hkv, self.d, self.dtype = B, H, Hkv, d, dtype
+        self.page_size, self.num_pages, self.max_pages = page_size, num_pages, max_pages
+        self.shape, self.strides = (num_pages, Hkv, page_size, d), tuple(int(x) for x in strides)
+        self.code = {"bf16": FS_BF16, "f32": FS_F32, "f16": FS_F16}[dtype]
+        self.c = FsPagedParams(B, H, Hkv, d, page_size, num_pages, max_pages, *self.strides, self.code)
+        paged_workspace_size(self)             # refuses what is not supported
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def paged_workspace_size(params):
+    n = ctypes.c_size_t()
+    _check(load().fs_paged_workspace_size(params.ref(), ctypes.byref(n)), "fs_paged_workspace_size")
+    return n.value
+
+
+def alloc_paged_workspace(params, device="cuda"):
+    """A zero-filled workspace for the paged calls (its flag and counters must start at zero)."""
+    import torch
+    return torch.zeros(paged_workspace_size(params), dtype=torch.uint8, device=device)
+
+
+def alloc_pages(params, device="cuda"):
+    """An empty cache: pools Kp, Vp (contents undefined), refs, table and lens."""
+    import torch
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32, "f16": torch.float16}[params.dtype]
+    size = sum((n - 1) * s for n, s in zip(params.shape, params.strides)) + params.d
+    Kp, Vp = (torch.empty(size, dtype=dt, device=device).as_strided(params.shape, params.strides + (1,))
+              for _ in range(2))
+    refs = torch.zeros(params.num_pages, dtype=torch.int32, device=device)
+    table = torch.full((params.B, params.max_pages), -1, dtype=torch.int32, device=device)
+    return Kp, Vp, refs, table, torch.zeros(params.B, dtype=torch.int32, device=device)
+
+
+def _pools(p, where, *pools):
+    for t in pools:
+        st = t.stride()
+        _need(tuple(t.shape) == p.shape and _dtype(t, where) == p.code and st[3] == 1 and
+              all(n == 1 or a == b for n, a, b in zip(p.shape, st, p.strides)), where,
+              "pools have the type, shape and strides of the parameters")
+
+
+def _ints(where, shape, *tensors):
+    import torch
+    for t in tensors:
+        _need(t.dtype is torch.int32 and tuple(t.shape) == shape and t.is_contiguous(), where,
+              "index arrays are contiguous int32 of the stated shape %s" % (shape,))
+
+
+def _rows(p, where, t, heads, rows):
+    """A [rows, heads, d] tensor with heads d apart: its row stride."""
+    st = t.stride()
+    _need(tuple(t.shape) == (rows, heads, p.d) and _dtype(t, where) == p.code and st[2] == 1 and
+          (heads == 1 or st[1] == p.d), where, "rows are [%d, %d, %d] of the cache's type, heads contiguous" %
+          (rows, heads, p.d))
+    return st[0]
+
+
+def paged_append(params, K_new, V_new, Kp, Vp, table, lens, ws, cu=None, rotary=None, Q=None, Qo=None, stream=None):
+    """Writes the newest tokens into their pages: K_new, V_new [T, Hkv, d]; sequence b's are the
+    rows cu[b] .. cu[b+1]-1 at its last positions (cu None: row b at lens[b] - 1).  With `rotary`
+    the keys are rotated on the way and Q [T, H, d] into Qo."""
+    where, p, T = "fs_paged_append", params, K_new.shape[0]
+    ks, vs = _rows(p, where, K_new, p.Hkv, T), _rows(p, where, V_new, p.Hkv, T)
+    _need((Q is None) == (Qo is None), where, "Q and Qo come together")
+    qs, qos = (0, 0) if Q is None else (_rows(p, where, Q, p.H, T), _rows(p, where, Qo, p.H, T))
+    _pools(p, where, Kp, Vp)
+    _ints(where, (p.B, p.max_pages), table)
+    _ints(where, (p.B,), lens)
+    ts = [K_new, V_new, Kp, Vp, table, lens, ws] + ([Q, Qo] if Q is not None else [])
+    if cu is not None:
+        _ints(where, (p.B + 1,), cu)
+        ts.append(cu)
+    with _On(where, stream, *ts) as st:
+        _check(load().fs_paged_append(p.ref(), None if rotary is None else rotary.ref(), T, _ptr(Q), qs, _ptr(Qo), qos,
+                                      K_new.data_ptr(), ks, V_new.data_ptr(), vs, _ptr(cu), Kp.data_ptr(),
+                                      Vp.data_ptr(), table.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.nbytes, st),
+               where)
+
+
+def paged_attend(params, Q, Kp, Vp, table, lens, O, ws, lse=None, window=-1, scale=None, stream=None):
+    """O [B, H, d] = attention of each sequence's newest token, query row Q[b], over its pages: all
+    of them, or the last window + 1 tokens.  scale None: 1/sqrt(d).  lse: optional float32 [B, H]."""
+    where, p = "fs_paged_attend", params
+    qs, os_ = _rows(p, where, Q, p.H, p.B), _rows(p, where, O, p.H, p.B)
+    _pools(p, where, Kp, Vp)
+    _ints(where, (p.B, p.max_pages), table)
+    _ints(where, (p.B,), lens)
+    ts = [Q, Kp, Vp, table, lens, O, ws]
+    if lse is not None:
+        _need(_dtype(lse, where) == FS_F32 and tuple(lse.shape) == (p.B, p.H) and lse.is_contiguous(), where,
+              "lse is float32 [B, H]")
+        ts.append(lse)
+    with _On(where, stream, *ts) as st:
+        _check(load().fs_paged_attend(p.ref(), Q.data_ptr(), qs, Kp.data_ptr(), Vp.data_ptr(), table.data_ptr(),
+                                      lens.data_ptr(), int(window), p.d ** -0.5 if scale is None else float(scale),
+                                      O.data_ptr(), os_, _ptr(lse), ws.data_ptr(), ws.nbytes, st), where)
+
+
+def pages_reserve(params, n_new, refs, table, lens, ws, stream=None):
+    """Room for n_new[b] (int32) more tokens of every sequence; lens grows by them."""
+    where, p = "fs_pages_reserve", params
+    _ints(where, (p.B,), n_new, lens)
+    _ints(where, (p.num_pages,), refs)
+    _ints(where, (p.B, p.max_pages), table)
+    with _On(where, stream, n_new, refs, table, lens, ws) as st:
+        _check(load().fs_pages_reserve(p.ref(), n_new.data_ptr(), refs.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                                       ws.data_ptr(), ws.nbytes, st), where)
+
+
+def pages_copy(params, Kp, Vp, src, dst, ws, stream=None):
+    """Page dst[i] of both pools becomes a copy of page src[i] (int32)."""
+    where, p = "fs_pages_copy", params
+    _pools(p, where, Kp, Vp)
+    _ints(where, (src.numel(),), src, dst)
+    with _On(where, stream, Kp, Vp, src, dst, ws) as st:
+        _check(load().fs_pages_copy(p.ref(), Kp.data_ptr(), Vp.data_ptr(), src.data_ptr(), dst.data_ptr(), src.numel(),
+                                    ws.data_ptr(), ws.nbytes, st), where)
+
+
+def pages_fork(params, Kp, Vp, refs, table, lens, src, dst, ws, stream=None):
+    """The empty sequences dst[i] become branches of src[i] (int32): whole pages shared, a
+    part-filled last page copied."""
+    where, p = "fs_pages_fork", params
+    _pools(p, where, Kp, Vp)
+    _ints(where, (p.num_pages,), refs)
+    _ints(where, (p.B, p.max_pages), table)
+    _ints(where, (p.B,), lens)
+    _ints(where, (src.numel(),), src, dst)
+    with _On(where, stream, Kp, Vp, refs, table, lens, src, dst, ws) as st:
+        _check(load().fs_pages_fork(p.ref(), Kp.data_ptr(), Vp.data_ptr(), refs.data_ptr(), table.data_ptr(),
+                                    lens.data_ptr(), src.data_ptr(), dst.data_ptr(), src.numel(), ws.data_ptr(),
+                                    ws.nbytes, st), where)
+
+
+def pages_free(params, refs, table, lens, rows, ws, stream=None):
+    """The sequences rows[i] (int32) give their pages back and are empty."""
+    where, p = "fs_pages_free", params
+    _ints(where, (p.num_pages,), refs)
+    _ints(where, (p.B, p.max_pages), table)
+    _ints(where, (p.B,), lens)
+    _ints(where, (rows.numel(),), rows)
+    with _On(where, stream, refs, table, lens, rows, ws) as st:
+        _check(load().fs_pages_free(p.ref(), refs.data_ptr(), table.data_ptr(), lens.data_ptr(), rows.data_ptr(),
+                                    rows.numel(), ws.data_ptr(), ws.nbytes, st), where)
+
+
+def pages_compact(params, Kp, Vp, refs, table, ws, live=None, refs_out=None, table_out=None, stream=None):
+    """Packs the pages in use to the pool's front.  refs and table are rewritten, or refs_out and
+    table_out receive the packed cache's; live (int32 [1]) receives the number of pages in use."""
+    where, p = "fs_pages_compact", params
+    refs_out, table_out = refs if refs_out is None else refs_out, table if table_out is None else table_out
+    _pools(p, where, Kp, Vp)
+    _ints(where, (p.num_pages,), refs, refs_out)
+    _ints(where, (p.B, p.max_pages), table, table_out)
+    ts = [Kp, Vp, refs, table, refs_out, table_out, ws]
+    if live is not None:
+        _ints(where, (1,), live)
+        ts.append(live)
+    with _On(where, stream, *ts) as st:
+        _check(load().fs_pages_compact(p.ref(), Kp.data_ptr(), Vp.data_ptr(), refs.data_ptr(), table.data_ptr(),
+                                       refs_out.data_ptr(), table_out.data_ptr(), _ptr(live), ws.data_ptr(), ws.nbytes,
+                                       st), where)
+
+
 # ---- diagnostics -------------------------------------------------------------------
 def launch_count():
     """Kernels the library has launched since it was loaded."""
@@ -351,7 +669,7 @@ def timing_enable(on=True):
 
 def kernel_times():
     """{kernel name: (launches, summed device ms)} since the previous read (then cleared)."""
-    n = 32
+    n = 64
     cnt = (ctypes.c_longlong * n)()
     ms = (ctypes.c_double * n)()
     k = load().fs_kernel_times(n, cnt, ms)

@@ -138,7 +138,9 @@ enum KernelId : int {
     kSummaries = 0, kExitTimes, kSelect, kReadout, kWindow, kRopeTable, kWindowTc, kAttnTc,
     kSelectTc, kRopeKeys, kCacheAppend, kCacheAttend, kRerank, kIdxTiles, kBwdRotate, kBwdRows,
     kBwdWindowKv, kBwdCells, kBwdReadoutKv, kBwdDalpha, kTreePrep, kTreeMerge, kTreeNodes, kTreeSearch,
-    kBwdLrRows, kRerankTc, kReadoutRows, kTileLists, kBwdReadoutTc, kBwdWindowTc, kNumKernels
+    kBwdLrRows, kRerankTc, kReadoutRows, kTileLists, kBwdReadoutTc, kBwdWindowTc,
+    kRope, kPagedAppend, kPagedAttend, kPagesReserve, kPagesCopy, kPagesForkPlan, kPagesFork, kPagesFree,
+    kPagesCompactPlan, kPagesCompact, kNumKernels
 };
 
 // Brackets one kernel launch: counts it and, when timing is on, records events around it.

@@ -36,7 +36,10 @@ const char *const kNames[kNumKernels] = {"cell_summaries", "exit_times", "select
                                          "bwd_rotate", "bwd_win_rows", "bwd_window_kv", "bwd_cells",
                                          "bwd_readout_kv", "bwd_dalpha", "tree_prep", "tree_merge",
                                          "tree_nodes", "tree_search", "bwd_lr_rows", "rerank_tc", "readout_rows",
-                                         "tile_lists", "bwd_readout_tc", "bwd_window_tc"};
+                                         "tile_lists", "bwd_readout_tc", "bwd_window_tc", "rope",
+                                         "paged_append", "paged_attend", "pages_reserve", "pages_copy",
+                                         "pages_fork_plan", "pages_fork", "pages_free", "pages_compact_plan",
+                                         "pages_compact"};
 }  // namespace
 
 LaunchScope::LaunchScope(int id_, cudaStream_t st_) : id(id_), st(st_), slot(-1) {

@@ -1,0 +1,190 @@
+// Writing new tokens into the paged cache (fs_paged_append): the queries and keys of a step or
+// of prompts are rotated by their positions, and keys and values go to their pages, in one
+// launch.  Every element is read once and written once; HBM bounds prompts, the launch and one
+// chain of loads (lens, table, rows) bound a decoding step.
+//
+// One thread holds one unit (16 bytes, 32 in the half layout) of a token's row and goes through
+// `hc` of its rows: query heads, key heads, value heads.  The position's sines and the page are
+// found once for all of them.
+#include "fs_paged.cuh"
+
+namespace fs {
+namespace {
+
+struct AppendArgs {
+    RotaryDev rot;
+    PagedDev P;
+    int T, Hq, Htot, units, nrot, hc;
+    long long qs, qos, ks, vs;                 // row strides in elements
+    const int32_t *cu, *table, *lens;
+    int *flag;
+};
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendAhead = 4;                // rows in flight per thread
+
+template <typename T, int VE, bool HALF>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs A, const T *Q, T *Qo,
+                                                                const T *__restrict__ Kn, const T *__restrict__ Vn,
+                                                                T *Kp, T *Vp) {
+    using Unit = RowUnit<T, VE, HALF>;
+    __shared__ int s_lo, s_hi;
+    griddep_wait();
+    const PagedDev &P = A.P;
+    const int per = kAppendThreads / A.units;  // tokens per block
+    const int lt = threadIdx.x / A.units, u = threadIdx.x - lt * A.units;
+    const int t0 = blockIdx.x * per, t = t0 + lt;
+
+    // the sequence of the block's first token: the interval of cu that holds it, cut into 256
+    // parts at a time, each thread testing one
+    int b = t;
+    if (A.cu) {
+        const int total = __ldg(A.cu + P.B);
+        if (t0 >= total) return;               // padding, the whole block
+        if (threadIdx.x == 0) {
+            s_lo = 0;
+            s_hi = P.B;
+        }
+        __syncthreads();
+        int lo = 0, hi = P.B;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + kAppendThreads - 1) / kAppendThreads;
+            const long long a = lo + (long long)threadIdx.x * step;
+            if (a < hi) {
+                const int e = (int)min(a + step, (long long)hi);
+                if (__ldg(A.cu + a) <= t0 && t0 < __ldg(A.cu + e)) {
+                    s_lo = (int)a;
+                    s_hi = e;
+                }
+            }
+            __syncthreads();
+            const int nlo = s_lo, nhi = s_hi;
+            __syncthreads();
+            // no part holds it: a padding row, or a cu that is not in order
+            if (nlo == lo && nhi == hi) break;
+            lo = nlo;
+            hi = nhi;
+        }
+        b = lo;
+        while (t < total && b + 1 < P.B && t >= __ldg(A.cu + b + 1)) b++;
+    }
+    if (lt >= per || t >= A.T) return;
+
+    int len = __ldg(A.lens + b), pos = len - 1;
+    if (A.cu) {
+        const int c0 = __ldg(A.cu + b), c1 = __ldg(A.cu + b + 1);
+        if (t < c0 || t >= c1) return;         // padding
+        pos = (int)max((long long)len - c1 + t, -1ll);
+    } else if (len == 0) {
+        return;
+    }
+    if (len > P.cap || pos < 0 || pos >= len) {
+        raise_check(A.flag);
+        return;
+    }
+    int pi, slot;
+    P.locate(pos, pi, slot);
+    const int page = __ldg(A.table + (long long)b * P.max_pages + pi);
+    if (!P.page_ok(page)) {
+        raise_check(A.flag);
+        return;
+    }
+    const long long at = page * P.sp + slot * P.st;
+    float c[Unit::kPairs], s[Unit::kPairs];
+    if (u < A.nrot)
+#pragma unroll
+        for (int m = 0; m < Unit::kPairs; m++)
+            rotary_angle(A.rot.turns[Unit::pair(u, m)], pos, A.rot.mscale, 1.f, c[m], s[m]);
+
+    const int d = P.d, h0 = blockIdx.y * A.hc, h1 = min(h0 + A.hc, A.Htot);
+    for (int g = h0; g < h1; g += kAppendAhead) {
+        Unit x[kAppendAhead];
+#pragma unroll
+        for (int j = 0; j < kAppendAhead; j++) {
+            const int h = g + j, hk = h - A.Hq, hv = hk - P.Hkv;
+            if (h < h1)
+                x[j].load(hk < 0 ? Q + t * A.qs + h * d : hv < 0 ? Kn + t * A.ks + hk * d : Vn + t * A.vs + hv * d, u, d,
+                          A.rot.r, A.nrot);
+        }
+#pragma unroll
+        for (int j = 0; j < kAppendAhead; j++) {
+            const int h = g + j, hk = h - A.Hq, hv = hk - P.Hkv;
+            if (h >= h1) continue;
+            if (u < A.nrot && hv < 0) x[j].turn(c, s);
+            x[j].store(hk < 0 ? Qo + t * A.qos + h * d : hv < 0 ? Kp + at + hk * P.sh : Vp + at + hv * P.sh, u, d,
+                       A.rot.r, A.nrot);
+        }
+    }
+}
+
+template <typename T, int VE, bool HALF>
+cudaError_t launch_as(AppendArgs &A, const void *Q, void *Qo, const void *Kn, const void *Vn, void *Kp, void *Vp,
+                      cudaStream_t st) {
+    using Unit = RowUnit<T, VE, HALF>;
+    A.nrot = Unit::rot_units(A.rot.r);
+    A.units = Unit::units(A.P.d, A.rot.r);
+    const int per = kAppendThreads / A.units;
+    // rows per thread: as many as leave two threads for every one that the GPU holds at once
+    // (148 x 2048), else one each, for latency
+    A.hc = 16;
+    while (A.hc > 1 && (long long)A.T * A.units * ((A.Htot + A.hc - 1) / A.hc) < 2ll * 148 * 2048) A.hc >>= 1;
+    LaunchScope scope(kPagedAppend, st);
+    return launch_pdl(append_kernel<T, VE, HALF>, dim3((unsigned)((A.T + per - 1) / per), (A.Htot + A.hc - 1) / A.hc),
+                      dim3(kAppendThreads), 0, st, A, (const T *)Q, (T *)Qo, (const T *)Kn, (const T *)Vn, (T *)Kp,
+                      (T *)Vp);
+}
+
+template <typename T>
+cudaError_t launch_append(AppendArgs &A, bool half, const void *Q, void *Qo, const void *Kn, const void *Vn, void *Kp,
+                          void *Vp, cudaStream_t st) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool vec = (half ? A.rot.r / 2 : A.rot.r) % V == 0;      // else a vector would hold parts of two pairs' halves
+    if (vec)
+        return half ? launch_as<T, V, true>(A, Q, Qo, Kn, Vn, Kp, Vp, st)
+                    : launch_as<T, V, false>(A, Q, Qo, Kn, Vn, Kp, Vp, st);
+    return half ? launch_as<T, 1, true>(A, Q, Qo, Kn, Vn, Kp, Vp, st)
+                : launch_as<T, 1, false>(A, Q, Qo, Kn, Vn, Kp, Vp, st);
+}
+
+}  // namespace
+}  // namespace fs
+
+using namespace fs;
+
+extern "C" fs_status fs_paged_append(const fs_paged_params *p, const fs_rotary *rot, int T, const void *Q,
+                                     long long q_stride, void *Qo, long long qo_stride, const void *K_new,
+                                     long long k_stride, const void *V_new, long long v_stride, const int32_t *cu,
+                                     void *Kp, void *Vp, const int32_t *table, const int32_t *lens, void *ws,
+                                     size_t ws_bytes, void *stream) {
+    AppendArgs A;
+    const fs_status s = paged_call(p, &A.P, ws, ws_bytes);
+    if (s != FS_OK) return s;
+    if (T < 0 || (!cu && T != p->B)) return FS_ERR_INVALID_ARG;
+    if (Q && (!Qo || !rot)) return FS_ERR_INVALID_ARG;         // without a rotation there is nothing to do to Q
+    if (Q && Q == Qo && q_stride != qo_stride) return FS_ERR_INVALID_ARG;
+    A.rot.r = 0;
+    if (rot) {
+        const fs_status r = rotary_dev(rot, p->d, &A.rot);
+        if (r != FS_OK) return r;
+    }
+    if (T == 0) return FS_OK;
+    if (!K_new || !V_new || !Kp || !Vp || !table || !lens) return FS_ERR_INVALID_ARG;
+    const long long v = 16 / (long long)dtype_bytes(p->dtype);
+    if (!aligned16(Q) || !aligned16(Qo) || !aligned16(K_new) || !aligned16(V_new) || !aligned16(Kp) || !aligned16(Vp))
+        return FS_ERR_INVALID_ARG;
+    if (T > 1 && ((Q && (q_stride % v || qo_stride % v)) || k_stride % v || v_stride % v)) return FS_ERR_UNSUPPORTED;
+    if (T > 1 && Q && qo_stride < (long long)p->H * p->d) return FS_ERR_INVALID_ARG;      // rows of Qo would overlap
+    A.T = T;
+    A.Hq = Q ? p->H : 0;
+    A.Htot = A.Hq + 2 * p->Hkv;
+    A.qs = q_stride; A.qos = qo_stride; A.ks = k_stride; A.vs = v_stride;
+    A.cu = cu; A.table = table; A.lens = lens;
+    A.flag = static_cast<int *>(ws);
+    const bool half = rot && rot->layout == FS_ROPE_HALF;
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (p->dtype == FS_BF16) e = launch_append<__nv_bfloat16>(A, half, Q, Qo, K_new, V_new, Kp, Vp, st);
+    else if (p->dtype == FS_F16) e = launch_append<__half>(A, half, Q, Qo, K_new, V_new, Kp, Vp, st);
+    else e = launch_append<float>(A, half, Q, Qo, K_new, V_new, Kp, Vp, st);
+    return e == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}

@@ -1,0 +1,696 @@
+// Attention of one new token per sequence over the paged cache (fs_paged_attend).
+//
+//     o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m),  one pass with a running m,
+//
+// for the H / Hkv query heads of a key-value head at once, so that K and V are read once: 4 d
+// flops a head and token against 2 d loads.  HBM bounds it (at 16 heads a group the tensor
+// cores are still below a tenth of what they give), for few tokens the chain of loads
+// lens -> table -> rows.
+//
+// Split.  The rows of work are (sequence, key-value head, tile of query heads).  Their tokens
+// are cut into tiles, the tiles of all rows are laid end to end, and every CTA of one resident
+// wave takes an equal share of them, found on the device from lens: ragged batches are spread
+// evenly, and the launch does not depend on lens, so a captured graph serves every step.  A row
+// that crosses CTAs is joined by the last of them to arrive, in the order of the CTAs, so the
+// result does not depend on who that is.
+//
+// Within a CTA each of four warps streams chunks of its own through a ring of three stages
+// (cp.async, 16 bytes a lane, the rows found through the page table one stage ahead) and keeps
+// its own m, sum and accumulators: no barrier until the row ends.
+//
+// bf16 and f16: S^T = K Q^T with 16 keys as the M and 8 heads as the N of mma.sync, then
+// O^T = V^T P^T, so a group of at most 8 heads wastes no rows of a 16-row tile, and the
+// probabilities become the second product's operand by an in-register 8x8 transpose.  The
+// tcgen05 form of these products would want 128 keys against at least 8 columns and the scores
+// brought back from tensor memory for each; at a tenth of the tensor rate it has nothing to
+// win, and its operands could not be read in pages of any size.
+// f32: a lane (or two, or four) per key for the scores, lanes over d for the values, fp32 FMA.
+#include "fs_paged.cuh"
+
+namespace fs {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 3;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+struct AttendArgs {
+    PagedDev P;
+    int G, NG, window;                         // heads per group, head tiles per group
+    float scale2;                              // scale * log2 e
+    long long qs, os;
+    const int32_t *table, *lens;
+    int *flag, *count;
+    float *part;
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes to shared memory; zeros where !ok (the source is then not read)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <typename T> struct Half2;
+template <> struct Half2<__nv_bfloat16> {
+    __device__ __forceinline__ static uint32_t pack(float a, float b) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    __device__ __forceinline__ static void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+template <> struct Half2<__half> {
+    __device__ __forceinline__ static uint32_t pack(float a, float b) {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    __device__ __forceinline__ static void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+
+// Sizes of one instantiation: HT query heads a tile.
+template <typename T, int D, int HT> struct Shape {
+    static constexpr bool kTc = sizeof(T) == 2;
+    static constexpr int kKeys = kTc ? (D == 64 ? 32 : 16) : (D == 64 ? 16 : 8);   // keys of a warp's chunk
+    static constexpr int kTile = kWarps * kKeys;                                   // tokens of a tile
+    static constexpr int kRowBytes = D * (int)sizeof(T);
+    static constexpr int kChunkBytes = 2 * kKeys * kRowBytes;                      // K and V
+    static constexpr int kWarpBytes = kStages * kChunkBytes;
+    static constexpr int kOutRow = D + 4;                                          // floats; spreads the banks
+    static constexpr int kSmem = kWarps * kWarpBytes;
+    static constexpr int kPart = HT * D + (HT == 1 ? 4 : 2 * HT);                   // floats of a partial result
+    static constexpr int kBlocks = kSmem > 110 * 1024 ? 1 : 2;                     // CTAs per SM
+    static_assert(kPart % 4 == 0 && kPart <= 16 * (D + 2), "16-byte vectors, attend_area_bytes");
+    static_assert(HT * kOutRow * 4 <= kWarpBytes, "a warp's result fits in its stages");
+};
+
+// Where a warp's chunk rows are: lane j < kKeys finds row j, one stage ahead of its use.
+template <int KEYS> struct Rows {
+    int page, slot;
+    bool in;
+    __device__ __forceinline__ void find(const PagedDev &P, const int32_t *trow, int tok0, int end, int lane) {
+        const int tok = tok0 + lane;
+        in = lane < KEYS && tok < end;
+        page = slot = 0;
+        if (in) {
+            int pi;
+            P.locate(tok, pi, slot);
+            page = __ldg(trow + pi);
+        }
+    }
+};
+
+// The chunk's rows of K and V to shared memory, 16 bytes a lane; 16-byte column c of row j lies
+// at column c ^ (j & 7), so eight rows' columns are in different banks.
+template <typename T, int D, int HT>
+__device__ __forceinline__ void fetch(const Rows<Shape<T, D, HT>::kKeys> &R, const AttendArgs &A, const T *Kh,
+                                      const T *Vh, uint32_t stage, int lane) {
+    using S = Shape<T, D, HT>;
+    constexpr int kCols = S::kRowBytes / 16;
+    const bool ok = R.in && A.P.page_ok(R.page);
+    if (R.in && !ok) raise_check(A.flag);
+    const long long off = ok ? R.page * A.P.sp + R.slot * A.P.st : -1;
+#pragma unroll
+    for (int i = 0; i < S::kKeys * kCols / 32; i++) {
+        const int x = i * 32 + lane, j = x / kCols, c = x % kCols;
+        const long long o = __shfl_sync(kFull, off, j);
+        const uint32_t dst = stage + j * S::kRowBytes + ((c ^ (j & 7)) << 4);
+        const long long e = (o < 0 ? 0 : o) + c * (16 / (int)sizeof(T));
+        cp16(dst, Kh + e, o >= 0);
+        cp16(dst + S::kKeys * S::kRowBytes, Vh + e, o >= 0);
+    }
+}
+
+// A warp's running softmax and accumulators, tensor-core form.  Lane l holds, for heads
+// 8 n + 2 (l % 4) + {0, 1}, the accumulator rows d = 16 t + l / 4 + {0, 8}.
+template <typename T, int D, int HT> struct TcState {
+    static constexpr int NT = HT / 8, DT = D / 16, MT = Shape<T, D, HT>::kKeys / 16;
+    uint32_t q[NT][DT][2];
+    float m[NT][2], l[NT][2], o[DT][NT][4];
+
+    // heads past the group's last are zeros and never written out
+    __device__ __forceinline__ void start(const T *Q, int heads, int lane) {
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const int h = 8 * n + lane / 4;
+            const uint32_t *row = reinterpret_cast<const uint32_t *>(Q + h * D);
+#pragma unroll
+            for (int t = 0; t < DT; t++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) q[n][t][e] = h < heads ? __ldg(row + 8 * t + 4 * e + lane % 4) : 0u;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int t = 0; t < DT; t++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) o[t][n][e] = 0.f;
+        }
+    }
+    // `left` keys of the chunk exist
+    __device__ __forceinline__ void chunk(uint32_t stage, int left, float scale2, int lane) {
+        using S = Shape<T, D, HT>;
+        float s[MT][NT][4];
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[i][n][e] = 0.f;
+            const int row = 16 * i + (lane & 15);
+            const uint32_t base = stage + row * S::kRowBytes;
+#pragma unroll
+            for (int t = 0; t < DT; t++) {
+                uint32_t a[4];
+                ldsm4(a, base + (((2 * t + (lane >> 4)) ^ (row & 7)) << 4));
+#pragma unroll
+                for (int n = 0; n < NT; n++) Half2<T>::mma(s[i][n], a, q[n][t][0], q[n][t][1]);
+            }
+        }
+        bool up = false;
+        float f[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                float x = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < MT; i++)
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        float &v = s[i][n][2 * k + e];
+                        v = 16 * i + 8 * k + lane / 4 < left ? v * scale2 : -INFINITY;
+                        x = fmaxf(x, v);
+                    }
+                x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+                const float top = fmaxf(m[n][e], x), ref = top == -INFINITY ? 0.f : top;
+                f[n][e] = exp2_fast(m[n][e] - ref);
+                up |= top != m[n][e];
+                m[n][e] = top;
+                l[n][e] *= f[n][e];
+#pragma unroll
+                for (int i = 0; i < MT; i++)
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        float &v = s[i][n][2 * k + e];
+                        v = exp2_fast(v - ref);
+                        l[n][e] += v;
+                    }
+            }
+        }
+        if (__any_sync(kFull, up)) {
+#pragma unroll
+            for (int t = 0; t < DT; t++)
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) o[t][n][e] *= f[n][e & 1];
+        }
+        // the probabilities are rounded to T for the product with V (half a step each, as random
+        // as the keys; their sum l keeps the fp32 values)
+        const uint32_t vbase = stage + S::kKeys * S::kRowBytes;
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) p[n][k] = transpose8(Half2<T>::pack(s[i][n][2 * k], s[i][n][2 * k + 1]));
+            const int row = 16 * i + (lane & 7) + ((lane >> 4) << 3);
+            const uint32_t base = vbase + row * S::kRowBytes;
+#pragma unroll
+            for (int t = 0; t < DT; t++) {
+                uint32_t a[4];
+                ldsm4t(a, base + (((2 * t + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
+#pragma unroll
+                for (int n = 0; n < NT; n++) Half2<T>::mma(o[t][n], a, p[n][0], p[n][1]);
+            }
+        }
+    }
+    // m, l and the accumulators to shared memory: out[head][D + 4]
+    __device__ __forceinline__ void finish(float *out, float *sm, float *sl, int lane) {
+        using S = Shape<T, D, HT>;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                float x = l[n][e];
+                x += __shfl_xor_sync(kFull, x, 4);
+                x += __shfl_xor_sync(kFull, x, 8);
+                x += __shfl_xor_sync(kFull, x, 16);
+                const int h = 8 * n + 2 * (lane % 4) + e;
+                if (lane < 4) {
+                    sm[h] = m[n][e];
+                    sl[h] = x;
+                }
+#pragma unroll
+                for (int t = 0; t < DT; t++) {
+                    out[h * S::kOutRow + 16 * t + lane / 4] = o[t][n][e];
+                    out[h * S::kOutRow + 16 * t + lane / 4 + 8] = o[t][n][e + 2];
+                }
+            }
+    }
+};
+
+// The same in fp32 FMA.  Scores: lane l takes key l % KEYS and every kParts-th 16-byte column
+// from l / KEYS on.  Values: lane l holds the d's of its 16-byte (D = 64: 8-byte) columns.
+template <int D, int HT> struct F32State {
+    using S = Shape<float, D, HT>;
+    static constexpr int KEYS = S::kKeys, kParts = 32 / KEYS, kCols = D / 4, kOwn = D / 32;
+    float m[HT], l[HT], o[HT][kOwn];
+
+    __device__ __forceinline__ void start() {
+#pragma unroll
+        for (int h = 0; h < HT; h++) {
+            m[h] = -INFINITY;
+            l[h] = 0.f;
+#pragma unroll
+            for (int e = 0; e < kOwn; e++) o[h][e] = 0.f;
+        }
+    }
+    // element offset in a row of the lane's own values (kOwn of them: 2, 4 or two times 4)
+    __device__ __forceinline__ static int own(int lane, int e) {
+        return kOwn == 2 ? 2 * lane + e : 4 * lane + (e & 3) + (e >> 2) * 128;
+    }
+    __device__ __forceinline__ void chunk(const uint8_t *stage, const float *sq, float *sp, int left, float scale2,
+                                          int lane) {
+        const int key = lane % KEYS, part = lane / KEYS;
+        float s[HT];
+#pragma unroll
+        for (int h = 0; h < HT; h++) s[h] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < kCols / kParts; i++) {
+            const int c = part + kParts * i;
+            const float4 k = *reinterpret_cast<const float4 *>(stage + key * S::kRowBytes + ((c ^ (key & 7)) << 4));
+#pragma unroll
+            for (int h = 0; h < HT; h++) {
+                const float4 q = *reinterpret_cast<const float4 *>(sq + h * D + 4 * c);
+                s[h] = fmaf(q.x, k.x, s[h]);
+                s[h] = fmaf(q.y, k.y, s[h]);
+                s[h] = fmaf(q.z, k.z, s[h]);
+                s[h] = fmaf(q.w, k.w, s[h]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < HT; h++) {
+#pragma unroll
+            for (int x = KEYS; x < 32; x <<= 1) s[h] += __shfl_xor_sync(kFull, s[h], x);
+            s[h] = key < left ? s[h] * scale2 : -INFINITY;
+            float x = s[h];
+#pragma unroll
+            for (int y = KEYS / 2; y >= 1; y >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, y));
+            const float top = fmaxf(m[h], x), ref = top == -INFINITY ? 0.f : top;
+            const float f = exp2f(m[h] - ref);
+            m[h] = top;
+            s[h] = exp2f(s[h] - ref);
+            l[h] = fmaf(l[h], f, s[h]);
+#pragma unroll
+            for (int e = 0; e < kOwn; e++) o[h][e] *= f;
+            if (part == 0) sp[key * HT + h] = s[h];
+        }
+        __syncwarp();
+        const uint8_t *v0 = stage + KEYS * S::kRowBytes;
+#pragma unroll 4
+        for (int k = 0; k < KEYS; k++) {
+            float v[kOwn];
+            if constexpr (kOwn == 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(v0 + k * S::kRowBytes + (((lane >> 1) ^ (k & 7)) << 4) +
+                                                                   (lane & 1) * 8);
+                v[0] = x.x; v[1] = x.y;
+            } else {
+#pragma unroll
+                for (int g = 0; g < kOwn / 4; g++) {
+                    const float4 x = *reinterpret_cast<const float4 *>(v0 + k * S::kRowBytes +
+                                                                       (((lane + 32 * g) ^ (k & 7)) << 4));
+                    v[4 * g] = x.x; v[4 * g + 1] = x.y; v[4 * g + 2] = x.z; v[4 * g + 3] = x.w;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < HT; h++) {
+                const float p = sp[k * HT + h];
+#pragma unroll
+                for (int e = 0; e < kOwn; e++) o[h][e] = fmaf(p, v[e], o[h][e]);
+            }
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void finish(float *out, float *sm, float *sl, int lane) {
+#pragma unroll
+        for (int h = 0; h < HT; h++) {
+            float x = l[h];
+#pragma unroll
+            for (int y = KEYS / 2; y >= 1; y >>= 1) x += __shfl_xor_sync(kFull, x, y);
+            if (lane == 0) {
+                sm[h] = m[h];
+                sl[h] = x;
+            }
+#pragma unroll
+            for (int e = 0; e < kOwn; e++) out[h * S::kOutRow + own(lane, e)] = o[h][e];
+        }
+    }
+};
+
+// Four consecutive outputs, rounded once.
+template <typename T> __device__ __forceinline__ void store4(T *p, float4 v, float f) {
+    Pack<T, 4> x;
+    x.e[0] = from_f<T>(v.x * f); x.e[1] = from_f<T>(v.y * f);
+    x.e[2] = from_f<T>(v.z * f); x.e[3] = from_f<T>(v.w * f);
+    *reinterpret_cast<Pack<T, 4> *>(p) = x;
+}
+__device__ __forceinline__ void add4(float4 &a, float f, const float4 &b) {
+    a.x = fmaf(f, b.x, a.x); a.y = fmaf(f, b.y, a.y); a.z = fmaf(f, b.z, a.z); a.w = fmaf(f, b.w, a.w);
+}
+
+template <typename T, int D, int HT>
+__global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
+    paged_attend_kernel(const __grid_constant__ AttendArgs A, const T *__restrict__ Q, const T *__restrict__ Kp,
+                        const T *__restrict__ Vp, T *__restrict__ O, float *__restrict__ lse) {
+    using S = Shape<T, D, HT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_m[kWarps][HT], s_l[kWarps][HT], s_f[HT];
+    __shared__ __align__(16) float s_q[S::kTc ? 1 : HT * D];
+    __shared__ float s_p[S::kTc ? 1 : kWarps * S::kKeys * HT];
+    __shared__ long long s_sum[kWarps], s_rem;
+    __shared__ int s_b, s_last;
+    const PagedDev &P = A.P;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int HG = P.Hkv * A.NG;
+    griddep_wait();
+
+    // tokens that sequence b attends to: [first, len); an empty one has a tile of its own, which
+    // writes its zeros
+    auto span = [&](int b, int &first) {
+        int n = __ldg(A.lens + b);
+        if (n < 0 || n > P.cap) {
+            raise_check(A.flag);
+            n = n < 0 ? 0 : P.cap;
+        }
+        first = A.window >= 0 ? max(0, n - 1 - A.window) : 0;
+        return n;
+    };
+    auto tiles_of = [&](int b) {
+        int first;
+        const int n = span(b, first);
+        return max(1, (n - first + S::kTile - 1) / S::kTile);
+    };
+
+    // this CTA's share [at, end) of all rows' tiles, and the sequence it begins in
+    const int seg = (P.B + kThreads - 1) / kThreads, b0 = min(P.B, tid * seg), b1 = min(P.B, b0 + seg);
+    long long mine = 0;
+    for (int b = b0; b < b1; b++) mine += tiles_of(b);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    total *= HG;
+    const long long per = (total + gridDim.x - 1) / gridDim.x;
+    const long long begin = blockIdx.x * per, end = min(total, begin + per);
+    if (begin >= end) return;
+    {
+        long long x = (before + incl - mine) * HG;
+        if (begin >= x && begin < x + mine * HG)
+            for (int b = b0; b < b1; b++) {
+                const long long n = (long long)tiles_of(b) * HG;
+                if (begin < x + n) {
+                    s_b = b;
+                    s_rem = begin - x;
+                    break;
+                }
+                x += n;
+            }
+    }
+    __syncthreads();
+    int b = s_b;
+    long long rem = s_rem, at = begin;         // tiles into sequence b, tiles into all
+
+    uint8_t *wsm = smem + warp * S::kWarpBytes;
+    const uint32_t wst = smem_addr(wsm);
+    while (at < end) {
+        int first;
+        const int n = span(b, first);
+        const int tiles = max(1, (n - first + S::kTile - 1) / S::kTile);
+        const int r = (int)(rem / tiles), tile = (int)(rem - (long long)r * tiles);
+        const int tile1 = (int)min((long long)tiles, tile + (end - at));
+        const int hkv = r / A.NG, h0 = hkv * A.G + (r - hkv * A.NG) * HT;      // first query head
+        const int heads = min(HT, (hkv + 1) * A.G - h0);
+        const int t0 = first + tile * S::kTile, t1 = min(n, first + tile1 * S::kTile);
+        const int chunks = max(0, (t1 - t0 + S::kKeys - 1) / S::kKeys);
+        const int cnt = (chunks - warp + kWarps - 1) / kWarps;                 // this warp's
+        const int32_t *trow = A.table + (long long)b * P.max_pages;
+        const T *Kh = Kp + hkv * P.sh, *Vh = Vp + hkv * P.sh;
+        const T *Qr = Q + b * A.qs + h0 * D;
+
+        auto tok0 = [&](int i) { return t0 + (warp + kWarps * i) * S::kKeys; };
+        Rows<S::kKeys> rows;
+        rows.find(P, trow, tok0(0), t1, lane);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; i++) {
+            if (i < cnt) fetch<T, D, HT>(rows, A, Kh, Vh, wst + i * S::kChunkBytes, lane);
+            cp_commit();
+            if (i + 1 < cnt) rows.find(P, trow, tok0(i + 1), t1, lane);
+        }
+        float *out = reinterpret_cast<float *>(wsm);
+        auto stream = [&](auto &&work) {
+            int slot = 0, fill = kStages - 1;
+            for (int i = 0; i < cnt; i++) {
+                cp_wait<kStages - 2>();
+                __syncwarp();
+                if (i + kStages - 1 < cnt) fetch<T, D, HT>(rows, A, Kh, Vh, wst + fill * S::kChunkBytes, lane);
+                cp_commit();
+                if (i + kStages < cnt) rows.find(P, trow, tok0(i + kStages), t1, lane);
+                work(slot * S::kChunkBytes, min(S::kKeys, t1 - tok0(i)));
+                slot = slot + 1 == kStages ? 0 : slot + 1;
+                fill = fill + 1 == kStages ? 0 : fill + 1;
+            }
+            cp_wait<0>();
+            __syncwarp();                      // the stages are free for the result
+        };
+        if constexpr (S::kTc) {
+            TcState<T, D, HT> st;
+            st.start(Qr, heads, lane);
+            stream([&](int off, int left) { st.chunk(wst + off, left, A.scale2, lane); });
+            st.finish(out, s_m[warp], s_l[warp], lane);
+        } else {
+            for (int x = tid; x < HT * D; x += kThreads) s_q[x] = x / D < heads ? (float)Qr[x] : 0.f;
+            __syncthreads();
+            F32State<D, HT> st;
+            st.start();
+            stream([&](int off, int left) {
+                st.chunk(wsm + off, s_q, s_p + warp * S::kKeys * HT, left, A.scale2, lane);
+            });
+            st.finish(out, s_m[warp], s_l[warp], lane);
+        }
+        __syncthreads();
+
+        // the four warps' results joined
+        const bool whole = tile == 0 && tile1 == tiles;
+        const long long row0 = at - tile;                                      // the row's first tile among all
+        float *part = A.part + ((long long)blockIdx.x * 2 + (tile == 0)) * S::kPart;
+        for (int x = tid; x < heads * (D / 4); x += kThreads) {
+            const int h = x / (D / 4), c = x % (D / 4) * 4;
+            float m = s_m[0][h], l = 0.f;
+#pragma unroll
+            for (int w = 1; w < kWarps; w++) m = fmaxf(m, s_m[w][h]);
+            const float ref = m == -INFINITY ? 0.f : m;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                const float f = exp2f(s_m[w][h] - ref);
+                l = fmaf(f, s_l[w][h], l);
+                add4(o, f, *reinterpret_cast<const float4 *>(smem + w * S::kWarpBytes + (h * S::kOutRow + c) * 4));
+            }
+            if (whole) {
+                store4(O + b * A.os + (h0 + h) * D + c, o, l == 0.f ? 0.f : 1.f / l);
+                if (lse && c == 0) lse[(long long)b * P.H + h0 + h] = (m + log2f(l)) * kLn2;
+            } else {
+                *reinterpret_cast<float4 *>(part + h * D + c) = o;
+                if (c == 0) {
+                    part[HT * D + h] = m;
+                    part[HT * D + HT + h] = l;
+                }
+            }
+        }
+        if (!whole) {
+            const int c0 = (int)(row0 / per), c1 = (int)((row0 + tiles - 1) / per);   // the CTAs of the row
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(A.count + c0, 1) == c1 - c0;
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                // c0 holds the row's beginning (its second part), the others continue it (their first)
+                auto at_part = [&](int i) { return A.part + ((long long)(c0 + i) * 2 + (i == 0)) * S::kPart; };
+                const int np = c1 - c0 + 1;
+                for (int h = warp; h < heads; h += kWarps) {
+                    float m = -INFINITY, l = 0.f;
+                    for (int i = lane; i < np; i += 32) m = fmaxf(m, __ldcg(at_part(i) + HT * D + h));
+                    m = warp_max(m);
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    for (int i = lane; i < np; i += 32)
+                        l = fmaf(exp2f(__ldcg(at_part(i) + HT * D + h) - ref), __ldcg(at_part(i) + HT * D + HT + h), l);
+                    l = warp_sum(l);
+                    if (lane == 0) {
+                        s_m[0][h] = ref;
+                        s_f[h] = l == 0.f ? 0.f : 1.f / l;
+                        if (lse) lse[(long long)b * P.H + h0 + h] = (m + log2f(l)) * kLn2;
+                    }
+                }
+                __syncthreads();
+                for (int x = tid; x < heads * (D / 4); x += kThreads) {
+                    const int h = x / (D / 4), c = x % (D / 4) * 4;
+                    const float ref = s_m[0][h];
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int i = 0; i < np; i++) {
+                        const float *p = at_part(i);
+                        add4(o, exp2f(__ldcg(p + HT * D + h) - ref), __ldcg(reinterpret_cast<const float4 *>(p + h * D + c)));
+                    }
+                    store4(O + b * A.os + (h0 + h) * D + c, o, s_f[h]);
+                }
+                if (tid == 0) A.count[c0] = 0;                                 // for the next call
+            }
+        }
+        __syncthreads();                       // the stages, s_m and s_l are free again
+        at += tile1 - tile;
+        rem += tile1 - tile;
+        if (rem == (long long)tiles * HG) {
+            rem = 0;
+            b++;
+        }
+    }
+}
+
+constexpr int kSms = 148;
+
+template <typename T, int D, int HT>
+cudaError_t launch_as(AttendArgs &A, const void *Q, const void *Kp, const void *Vp, void *O, float *lse,
+                      cudaStream_t st) {
+    using S = Shape<T, D, HT>;
+    A.NG = (A.G + HT - 1) / HT;
+    auto *kern = paged_attend_kernel<T, D, HT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    // one resident wave, or a CTA for every tile that the table could hold
+    const long long most = (long long)A.P.B * A.P.Hkv * A.NG *
+                           (((A.window >= 0 && A.window < A.P.cap ? A.window + 1 : A.P.cap) + S::kTile - 1) / S::kTile);
+    const int grid = (int)(most < kSms * S::kBlocks ? (most < 1 ? 1 : most) : kSms * S::kBlocks);
+    static_assert(kSms * 2 <= kPagedMaxCtas, "a counter for every CTA");
+    LaunchScope scope(kPagedAttend, st);
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), S::kSmem, st, A, (const T *)Q, (const T *)Kp, (const T *)Vp,
+                      (T *)O, lse);
+}
+
+// Heads per tile: the smallest that holds the group (fewer rows of zeros); larger groups take
+// several tiles, each of which reads K and V again, mostly from L2.
+template <typename T>
+cudaError_t launch_attend(AttendArgs &A, const void *Q, const void *Kp, const void *Vp, void *O, float *lse,
+                          cudaStream_t st) {
+    const int d = A.P.d, G = A.G;
+    if constexpr (sizeof(T) == 2) {
+        if (G <= 8) {
+            if (d == 64) return launch_as<T, 64, 8>(A, Q, Kp, Vp, O, lse, st);
+            if (d == 128) return launch_as<T, 128, 8>(A, Q, Kp, Vp, O, lse, st);
+            return launch_as<T, 256, 8>(A, Q, Kp, Vp, O, lse, st);
+        }
+        if (d == 64) return launch_as<T, 64, 16>(A, Q, Kp, Vp, O, lse, st);
+        if (d == 128) return launch_as<T, 128, 16>(A, Q, Kp, Vp, O, lse, st);
+        return launch_as<T, 256, 16>(A, Q, Kp, Vp, O, lse, st);
+    } else {
+        if (G == 1) {
+            if (d == 64) return launch_as<T, 64, 1>(A, Q, Kp, Vp, O, lse, st);
+            if (d == 128) return launch_as<T, 128, 1>(A, Q, Kp, Vp, O, lse, st);
+            return launch_as<T, 256, 1>(A, Q, Kp, Vp, O, lse, st);
+        }
+        if (G <= 4) {
+            if (d == 64) return launch_as<T, 64, 4>(A, Q, Kp, Vp, O, lse, st);
+            if (d == 128) return launch_as<T, 128, 4>(A, Q, Kp, Vp, O, lse, st);
+            return launch_as<T, 256, 4>(A, Q, Kp, Vp, O, lse, st);
+        }
+        if (d == 64) return launch_as<T, 64, 8>(A, Q, Kp, Vp, O, lse, st);
+        if (d == 128) return launch_as<T, 128, 8>(A, Q, Kp, Vp, O, lse, st);
+        return launch_as<T, 256, 8>(A, Q, Kp, Vp, O, lse, st);
+    }
+}
+
+}  // namespace
+
+// two partial results for every CTA, of at most 16 heads
+size_t attend_area_bytes(const fs_paged_params *p) { return (size_t)kSms * 2 * 2 * 16 * (p->d + 2) * 4; }
+
+}  // namespace fs
+
+using namespace fs;
+
+extern "C" fs_status fs_paged_attend(const fs_paged_params *p, const void *Q, long long q_stride, const void *Kp,
+                                     const void *Vp, const int32_t *table, const int32_t *lens, int window,
+                                     float scale, void *O, long long o_stride, float *lse, void *ws, size_t ws_bytes,
+                                     void *stream) {
+    AttendArgs A;
+    const fs_status s = paged_call(p, &A.P, ws, ws_bytes);
+    if (s != FS_OK) return s;
+    if (!Q || !Kp || !Vp || !table || !lens || !O) return FS_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || scale > 1e30f) return FS_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(O)) return FS_ERR_INVALID_ARG;
+    const long long v = 16 / (long long)dtype_bytes(p->dtype);
+    if (p->B > 1 && (q_stride % v || o_stride % v)) return FS_ERR_UNSUPPORTED;
+    if (p->B > 1 && o_stride < (long long)p->H * p->d) return FS_ERR_INVALID_ARG;        // rows of O would overlap
+    A.G = p->H / p->Hkv;
+    A.NG = 1;
+    A.window = window;
+    A.scale2 = scale * kLog2e;
+    A.qs = q_stride;
+    A.os = o_stride;
+    A.table = table;
+    A.lens = lens;
+    A.flag = static_cast<int *>(ws);
+    A.count = reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + kPagedCounters);
+    A.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kPagedArea);
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (p->dtype == FS_BF16) e = launch_attend<__nv_bfloat16>(A, Q, Kp, Vp, O, lse, st);
+    else if (p->dtype == FS_F16) e = launch_attend<__half>(A, Q, Kp, Vp, O, lse, st);
+    else e = launch_attend<float>(A, Q, Kp, Vp, O, lse, st);
+    return e == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}
