@@ -64,8 +64,10 @@ class FsRotary(ctypes.Structure):
 
 
 class FsRopeParams(ctypes.Structure):
+    # the strides q[3], qo[3], k[3], ko[3] field by field (quicker to fill than arrays)
     _fields_ = ([(n, ctypes.c_int) for n in ("B", "N", "H", "Hk", "d")] +
-                [(n, ctypes.c_longlong * 3) for n in ("q", "qo", "k", "ko")] + [("dtype", ctypes.c_int)])
+                [(t + "_" + x, ctypes.c_longlong) for t in ("q", "qo", "k", "ko") for x in "bhn"] +
+                [("dtype", ctypes.c_int)])
 
 
 class FsPagedParams(ctypes.Structure):
@@ -377,45 +379,57 @@ def cache_status(cache, stream=None):
 
 
 # ---- serving: what the calls below share ---------------------------------------------
-def _need(ok, where, what):
-    if not ok:
-        raise FsError(1, "%s: %s" % (where, what))
+# A decoding step makes a few of these calls, each a few microseconds on the GPU, so the checks
+# compare whole tuples first and look closer only where those differ.
+def _refuse(where, what):
+    raise FsError(1, "%s: %s" % (where, what))
+
+
+_torch = _raw_stream = None
+
+
+def _types():
+    """torch, once it is imported, and the element types of the serving calls."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        # the current stream's handle; the public call makes an object for it, 1.2 us
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _torch = torch
+        _DTYPES.update({torch.bfloat16: FS_BF16, torch.float32: FS_F32, torch.float16: FS_F16})
+    return _torch
 
 
 _DTYPES = {}
 
 
 def _dtype(t, where):
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.bfloat16: FS_BF16, torch.float32: FS_F32, torch.float16: FS_F16})
+    if _torch is None:
+        _types()
     code = _DTYPES.get(t.dtype)
-    _need(code is not None, where, "tensors are bf16, f16 or f32")
+    if code is None:
+        _refuse(where, "tensors are bf16, f16 or f32")
     return code
 
 
-class _On:
-    """The device of a call's tensors made current, and its stream (the current one unless given)."""
-
-    def __init__(self, where, stream, *tensors):
-        import torch
-        self.dev = dev = tensors[0].device
-        _need(dev.type == "cuda", where, "tensors are on a CUDA device")
-        for t in tensors:
-            _need(t.device == dev, where, "all tensors are on one device")
-        self.stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-        self.was = torch.cuda.current_device()
-
-    def __enter__(self):
-        if self.was != self.dev.index:
-            import torch
-            torch.cuda.set_device(self.dev)
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.was != self.dev.index:
-            import torch
-            torch.cuda.set_device(self.was)
+def _run(fn, where, stream, tensors, *args):
+    """fn(*args, stream) with the tensors' device current; on that device's current stream unless given."""
+    torch = _torch or _types()
+    dev = tensors[0].get_device()
+    if dev < 0:
+        _refuse(where, "tensors are on a CUDA device")
+    for t in tensors:
+        if t.get_device() != dev:
+            _refuse(where, "all tensors are on one device")
+    stream = _raw_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream)
+    if code:
+        raise FsError(code, where)
 
 
 # ---- rotary positions ----------------------------------------------------------------
@@ -428,7 +442,8 @@ class Rotary:
 
     def __init__(self, r, layout="interleaved", base=10000.0, scaling="none", factor=1.0, orig_len=0.0, slow=1.0,
                  fast=32.0, mscale=1.0):
-        _need(layout in self.LAYOUTS and scaling in self.SCALINGS, "Rotary", "layout or scaling unknown")
+        if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
+            _refuse("Rotary", "layout or scaling unknown")
         self.c = FsRotary()
         _check(load().fs_rotary_init(int(r), self.LAYOUTS[layout], base, self.SCALINGS[scaling], factor, orig_len,
                                      slow, fast, mscale, ctypes.byref(self.c)), "fs_rotary_init")
@@ -439,31 +454,34 @@ class Rotary:
 
 
 def _rope(fn, where, rotary, Q, Qo, K, Ko, positions, pos0, stream):
-    _need((K is None) == (Ko is None), where, "K and its output come together")
-    _need(Q.dim() == 4 and Q.shape == Qo.shape and Qo.dtype == Q.dtype, where, "Q and its output are [B,H,N,d]")
-    B, H, N, d = Q.shape
-    c = FsRopeParams()
-    c.B, c.N, c.H, c.d, c.dtype = B, N, H, d, _dtype(Q, where)
-    ts = [Q, Qo]
-    for t, s in ((Q, c.q), (Qo, c.qo)) if K is None else ((Q, c.q), (Qo, c.qo), (K, c.k), (Ko, c.ko)):
-        st = t.stride()
-        _need(d == 1 or st[3] == 1, where, "a row's elements are contiguous")
-        s[:] = st[:3]
-    if K is not None:
-        _need(K.dim() == 4 and K.shape == Ko.shape and K.dtype == Ko.dtype == Q.dtype and K.shape[0] == B and
-              K.shape[2] == N and K.shape[3] == d, where, "K and its output are [B,Hk,N,d] of Q's type")
-        c.Hk = K.shape[1]
+    shape = Q.shape
+    if len(shape) != 4 or Qo.shape != shape or Qo.dtype != Q.dtype:
+        _refuse(where, "Q and its output are [B,H,N,d] of one type")
+    B, H, N, d = shape
+    Hk, ts, ks_, kos = 0, [Q, Qo], (0, 0, 0, 1), (0, 0, 0, 1)
+    if K is not None and Ko is not None:
+        ks = K.shape
+        if len(ks) != 4 or Ko.shape != ks or not K.dtype == Ko.dtype == Q.dtype or (ks[0], ks[2], ks[3]) != (B, N, d):
+            _refuse(where, "K and its output are [B,Hk,N,d] of Q's type")
+        Hk, ks_, kos = ks[1], K.stride(), Ko.stride()
         ts += [K, Ko]
+    elif K is not None or Ko is not None:
+        _refuse(where, "K and its output come together")
+    qs, qos = Q.stride(), Qo.stride()
+    if d > 1 and not qs[3] == qos[3] == ks_[3] == kos[3] == 1:
+        _refuse(where, "a row's elements are contiguous")
     ps = 0
     if positions is not None:
-        _need(positions.dtype.itemsize == 4 and not positions.is_floating_point(), where, "positions are int32")
-        _need(tuple(positions.shape) in ((N,), (B, N)) and (N <= 1 or positions.stride(-1) == 1), where,
-              "positions are [N] or [B,N], a row contiguous")
-        ps = positions.stride(0) if positions.dim() == 2 else 0
+        if positions.dtype is not (_torch or _types()).int32:
+            _refuse(where, "positions are int32")
+        if positions.shape not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
+            _refuse(where, "positions are [N] or [B,N], a row contiguous")
+        if positions.dim() == 2:
+            ps = positions.stride(0)
         ts.append(positions)
-    with _On(where, stream, *ts) as st:
-        _check(fn(ctypes.byref(c), rotary.ref(), Q.data_ptr(), Qo.data_ptr(), _ptr(K), _ptr(Ko), _ptr(positions), ps,
-                  int(pos0), st), where)
+    c = FsRopeParams(B, N, H, Hk, d, qs[0], qs[1], qs[2], qos[0], qos[1], qos[2], ks_[0], ks_[1], ks_[2], kos[0], kos[1],
+                     kos[2], _dtype(Q, where))
+    _run(fn, where, stream, ts, c, rotary.c, Q.data_ptr(), Qo.data_ptr(), _ptr(K), _ptr(Ko), _ptr(positions), ps, int(pos0))
 
 
 def rope(rotary, Q, Qo, K=None, Ko=None, positions=None, pos0=0, stream=None):
@@ -486,14 +504,16 @@ class PagedParams:
 
     def __init__(self, *, B, H, Hkv, page_size, num_pages, max_pages, d=64, dtype="bf16", layout="heads_first",
                  strides=None):
-        _need(dtype in ("bf16", "f32", "f16") and layout in ("heads_first", "tokens_first"), "PagedParams",
-              "dtype or layout unknown")
+        if dtype not in ("bf16", "f32", "f16") or layout not in ("heads_first", "tokens_first"):
+            _refuse("PagedParams", "dtype or layout unknown")
         if strides is None:
             page = Hkv * page_size * d
             strides = (page, page_size * d, d) if layout == "heads_first" else (page, d, Hkv * d)
         self.B, self.H, self.Hkv, self.d, self.dtype = B, H, Hkv, d, dtype
         self.page_size, self.num_pages, self.max_pages = page_size, num_pages, max_pages
         self.shape, self.strides = (num_pages, Hkv, page_size, d), tuple(int(x) for x in strides)
+        self.scale = d ** -0.5 if d > 0 else 0.0
+        self.stride4, self.table_shape, self.table_stride = self.strides + (1,), (B, max_pages), (max_pages, 1)
         self.code = {"bf16": FS_BF16, "f32": FS_F32, "f16": FS_F16}[dtype]
         self.c = FsPagedParams(B, H, Hkv, d, page_size, num_pages, max_pages, *self.strides, self.code)
         paged_workspace_size(self)             # refuses what is not supported
@@ -528,25 +548,31 @@ def alloc_pages(params, device="cuda"):
 
 def _pools(p, where, *pools):
     for t in pools:
+        if t.shape != p.shape or _dtype(t, where) != p.code:
+            _refuse(where, "pools have the shape and type of the parameters")
         st = t.stride()
-        _need(tuple(t.shape) == p.shape and _dtype(t, where) == p.code and st[3] == 1 and
-              all(n == 1 or a == b for n, a, b in zip(p.shape, st, p.strides)), where,
-              "pools have the type, shape and strides of the parameters")
+        if st != p.stride4 and (st[3] != 1 or any(n > 1 and a != b for n, a, b in zip(p.shape, st, p.strides))):
+            _refuse(where, "pools have the strides of the parameters")
 
 
-def _ints(where, shape, *tensors):
-    import torch
+def _ints(where, n, *tensors):
+    int32 = (_torch or _types()).int32
     for t in tensors:
-        _need(t.dtype is torch.int32 and tuple(t.shape) == shape and t.is_contiguous(), where,
-              "index arrays are contiguous int32 of the stated shape %s" % (shape,))
+        if t.dtype is not int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+            _refuse(where, "a list is contiguous int32 of the length that goes with the others")
+
+
+def _table(p, where, t):
+    if t.dtype is not (_torch or _types()).int32 or t.shape != p.table_shape or not (
+            t.stride() == p.table_stride or t.is_contiguous()):
+        _refuse(where, "table is contiguous int32 [B, max_pages]")
 
 
 def _rows(p, where, t, heads, rows):
     """A [rows, heads, d] tensor with heads d apart: its row stride."""
     st = t.stride()
-    _need(tuple(t.shape) == (rows, heads, p.d) and _dtype(t, where) == p.code and st[2] == 1 and
-          (heads == 1 or st[1] == p.d), where, "rows are [%d, %d, %d] of the cache's type, heads contiguous" %
-          (rows, heads, p.d))
+    if t.shape != (rows, heads, p.d) or _dtype(t, where) != p.code or st[2] != 1 or (heads > 1 and st[1] != p.d):
+        _refuse(where, "rows are [rows, heads, d] of the cache's type and sizes, a row's heads contiguous")
     return st[0]
 
 
@@ -556,20 +582,21 @@ def paged_append(params, K_new, V_new, Kp, Vp, table, lens, ws, cu=None, rotary=
     the keys are rotated on the way and Q [T, H, d] into Qo."""
     where, p, T = "fs_paged_append", params, K_new.shape[0]
     ks, vs = _rows(p, where, K_new, p.Hkv, T), _rows(p, where, V_new, p.Hkv, T)
-    _need((Q is None) == (Qo is None), where, "Q and Qo come together")
-    qs, qos = (0, 0) if Q is None else (_rows(p, where, Q, p.H, T), _rows(p, where, Qo, p.H, T))
     _pools(p, where, Kp, Vp)
-    _ints(where, (p.B, p.max_pages), table)
-    _ints(where, (p.B,), lens)
-    ts = [K_new, V_new, Kp, Vp, table, lens, ws] + ([Q, Qo] if Q is not None else [])
+    _table(p, where, table)
+    _ints(where, p.B, lens)
+    ts, qs, qos = [K_new, V_new, Kp, Vp, table, lens, ws], 0, 0
+    if Q is not None and Qo is not None:
+        qs, qos = _rows(p, where, Q, p.H, T), _rows(p, where, Qo, p.H, T)
+        ts += [Q, Qo]
+    elif Q is not None or Qo is not None:
+        _refuse(where, "Q and Qo come together")
     if cu is not None:
-        _ints(where, (p.B + 1,), cu)
+        _ints(where, p.B + 1, cu)
         ts.append(cu)
-    with _On(where, stream, *ts) as st:
-        _check(load().fs_paged_append(p.ref(), None if rotary is None else rotary.ref(), T, _ptr(Q), qs, _ptr(Qo), qos,
-                                      K_new.data_ptr(), ks, V_new.data_ptr(), vs, _ptr(cu), Kp.data_ptr(),
-                                      Vp.data_ptr(), table.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.nbytes, st),
-               where)
+    _run(load().fs_paged_append, where, stream, ts, p.c, None if rotary is None else rotary.c, T, _ptr(Q), qs, _ptr(Qo),
+         qos, K_new.data_ptr(), ks, V_new.data_ptr(), vs, _ptr(cu), Kp.data_ptr(), Vp.data_ptr(), table.data_ptr(),
+         lens.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
 def paged_attend(params, Q, Kp, Vp, table, lens, O, ws, lse=None, window=-1, scale=None, stream=None):
@@ -578,65 +605,60 @@ def paged_attend(params, Q, Kp, Vp, table, lens, O, ws, lse=None, window=-1, sca
     where, p = "fs_paged_attend", params
     qs, os_ = _rows(p, where, Q, p.H, p.B), _rows(p, where, O, p.H, p.B)
     _pools(p, where, Kp, Vp)
-    _ints(where, (p.B, p.max_pages), table)
-    _ints(where, (p.B,), lens)
+    _table(p, where, table)
+    _ints(where, p.B, lens)
     ts = [Q, Kp, Vp, table, lens, O, ws]
     if lse is not None:
-        _need(_dtype(lse, where) == FS_F32 and tuple(lse.shape) == (p.B, p.H) and lse.is_contiguous(), where,
-              "lse is float32 [B, H]")
+        if _dtype(lse, where) != FS_F32 or lse.shape != (p.B, p.H) or not lse.is_contiguous():
+            _refuse(where, "lse is contiguous float32 [B, H]")
         ts.append(lse)
-    with _On(where, stream, *ts) as st:
-        _check(load().fs_paged_attend(p.ref(), Q.data_ptr(), qs, Kp.data_ptr(), Vp.data_ptr(), table.data_ptr(),
-                                      lens.data_ptr(), int(window), p.d ** -0.5 if scale is None else float(scale),
-                                      O.data_ptr(), os_, _ptr(lse), ws.data_ptr(), ws.nbytes, st), where)
+    _run(load().fs_paged_attend, where, stream, ts, p.c, Q.data_ptr(), qs, Kp.data_ptr(), Vp.data_ptr(),
+         table.data_ptr(), lens.data_ptr(), int(window), p.scale if scale is None else scale, O.data_ptr(), os_,
+         _ptr(lse), ws.data_ptr(), ws.nbytes)
 
 
 def pages_reserve(params, n_new, refs, table, lens, ws, stream=None):
     """Room for n_new[b] (int32) more tokens of every sequence; lens grows by them."""
     where, p = "fs_pages_reserve", params
-    _ints(where, (p.B,), n_new, lens)
-    _ints(where, (p.num_pages,), refs)
-    _ints(where, (p.B, p.max_pages), table)
-    with _On(where, stream, n_new, refs, table, lens, ws) as st:
-        _check(load().fs_pages_reserve(p.ref(), n_new.data_ptr(), refs.data_ptr(), table.data_ptr(), lens.data_ptr(),
-                                       ws.data_ptr(), ws.nbytes, st), where)
+    _ints(where, p.B, n_new, lens)
+    _ints(where, p.num_pages, refs)
+    _table(p, where, table)
+    _run(load().fs_pages_reserve, where, stream, (n_new, refs, table, lens, ws), p.c, n_new.data_ptr(), refs.data_ptr(),
+         table.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
 def pages_copy(params, Kp, Vp, src, dst, ws, stream=None):
     """Page dst[i] of both pools becomes a copy of page src[i] (int32)."""
-    where, p = "fs_pages_copy", params
+    where, p, n = "fs_pages_copy", params, src.numel()
     _pools(p, where, Kp, Vp)
-    _ints(where, (src.numel(),), src, dst)
-    with _On(where, stream, Kp, Vp, src, dst, ws) as st:
-        _check(load().fs_pages_copy(p.ref(), Kp.data_ptr(), Vp.data_ptr(), src.data_ptr(), dst.data_ptr(), src.numel(),
-                                    ws.data_ptr(), ws.nbytes, st), where)
+    _ints(where, n, src, dst)
+    _run(load().fs_pages_copy, where, stream, (Kp, Vp, src, dst, ws), p.c, Kp.data_ptr(), Vp.data_ptr(), src.data_ptr(),
+         dst.data_ptr(), n, ws.data_ptr(), ws.nbytes)
 
 
 def pages_fork(params, Kp, Vp, refs, table, lens, src, dst, ws, stream=None):
     """The empty sequences dst[i] become branches of src[i] (int32): whole pages shared, a
     part-filled last page copied."""
-    where, p = "fs_pages_fork", params
+    where, p, n = "fs_pages_fork", params, src.numel()
     _pools(p, where, Kp, Vp)
-    _ints(where, (p.num_pages,), refs)
-    _ints(where, (p.B, p.max_pages), table)
-    _ints(where, (p.B,), lens)
-    _ints(where, (src.numel(),), src, dst)
-    with _On(where, stream, Kp, Vp, refs, table, lens, src, dst, ws) as st:
-        _check(load().fs_pages_fork(p.ref(), Kp.data_ptr(), Vp.data_ptr(), refs.data_ptr(), table.data_ptr(),
-                                    lens.data_ptr(), src.data_ptr(), dst.data_ptr(), src.numel(), ws.data_ptr(),
-                                    ws.nbytes, st), where)
+    _ints(where, p.num_pages, refs)
+    _table(p, where, table)
+    _ints(where, p.B, lens)
+    _ints(where, n, src, dst)
+    _run(load().fs_pages_fork, where, stream, (Kp, Vp, refs, table, lens, src, dst, ws), p.c, Kp.data_ptr(),
+         Vp.data_ptr(), refs.data_ptr(), table.data_ptr(), lens.data_ptr(), src.data_ptr(), dst.data_ptr(), n,
+         ws.data_ptr(), ws.nbytes)
 
 
 def pages_free(params, refs, table, lens, rows, ws, stream=None):
     """The sequences rows[i] (int32) give their pages back and are empty."""
-    where, p = "fs_pages_free", params
-    _ints(where, (p.num_pages,), refs)
-    _ints(where, (p.B, p.max_pages), table)
-    _ints(where, (p.B,), lens)
-    _ints(where, (rows.numel(),), rows)
-    with _On(where, stream, refs, table, lens, rows, ws) as st:
-        _check(load().fs_pages_free(p.ref(), refs.data_ptr(), table.data_ptr(), lens.data_ptr(), rows.data_ptr(),
-                                    rows.numel(), ws.data_ptr(), ws.nbytes, st), where)
+    where, p, n = "fs_pages_free", params, rows.numel()
+    _ints(where, p.num_pages, refs)
+    _table(p, where, table)
+    _ints(where, p.B, lens)
+    _ints(where, n, rows)
+    _run(load().fs_pages_free, where, stream, (refs, table, lens, rows, ws), p.c, refs.data_ptr(), table.data_ptr(),
+         lens.data_ptr(), rows.data_ptr(), n, ws.data_ptr(), ws.nbytes)
 
 
 def pages_compact(params, Kp, Vp, refs, table, ws, live=None, refs_out=None, table_out=None, stream=None):
@@ -645,16 +667,15 @@ def pages_compact(params, Kp, Vp, refs, table, ws, live=None, refs_out=None, tab
     where, p = "fs_pages_compact", params
     refs_out, table_out = refs if refs_out is None else refs_out, table if table_out is None else table_out
     _pools(p, where, Kp, Vp)
-    _ints(where, (p.num_pages,), refs, refs_out)
-    _ints(where, (p.B, p.max_pages), table, table_out)
+    _ints(where, p.num_pages, refs, refs_out)
+    _table(p, where, table)
+    _table(p, where, table_out)
     ts = [Kp, Vp, refs, table, refs_out, table_out, ws]
     if live is not None:
-        _ints(where, (1,), live)
+        _ints(where, 1, live)
         ts.append(live)
-    with _On(where, stream, *ts) as st:
-        _check(load().fs_pages_compact(p.ref(), Kp.data_ptr(), Vp.data_ptr(), refs.data_ptr(), table.data_ptr(),
-                                       refs_out.data_ptr(), table_out.data_ptr(), _ptr(live), ws.data_ptr(), ws.nbytes,
-                                       st), where)
+    _run(load().fs_pages_compact, where, stream, ts, p.c, Kp.data_ptr(), Vp.data_ptr(), refs.data_ptr(),
+         table.data_ptr(), refs_out.data_ptr(), table_out.data_ptr(), _ptr(live), ws.data_ptr(), ws.nbytes)
 
 
 # ---- diagnostics -------------------------------------------------------------------

@@ -38,8 +38,8 @@ struct PagedDev {
 // calls for their lists.  Flag and counters lie at the same place whatever the parameters, so
 // a workspace made for the largest batch serves smaller ones.
 constexpr size_t kPagedCounters = 256;
-constexpr int kPagedMaxCtas = 1024;
-constexpr size_t kPagedArea = kPagedCounters + 4 * (size_t)kPagedMaxCtas;
+constexpr int kPagedCounts = 1024;
+constexpr size_t kPagedArea = kPagedCounters + 4 * (size_t)kPagedCounts;
 
 size_t attend_area_bytes(const fs_paged_params *p);
 size_t pages_area_bytes(const fs_paged_params *p);

@@ -21,13 +21,13 @@ struct AppendArgs {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendAhead = 4;                // rows in flight per thread
 
 template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs A, const T *Q, T *Qo,
+__global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_constant__ AppendArgs A, const T *Q, T *Qo,
                                                                 const T *__restrict__ Kn, const T *__restrict__ Vn,
                                                                 T *Kp, T *Vp) {
     using Unit = RowUnit<T, VE, HALF>;
+    constexpr int kAhead = HALF ? 2 : 4;       // rows in flight per thread: four vectors either way
     __shared__ int s_lo, s_hi;
     griddep_wait();
     const PagedDev &P = A.P;
@@ -96,24 +96,34 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         for (int m = 0; m < Unit::kPairs; m++)
             rotary_angle(A.rot.turns[Unit::pair(u, m)], pos, A.rot.mscale, 1.f, c[m], s[m]);
 
+    // this block's rows: some of the queries', then of the keys', then of the values'
     const int d = P.d, h0 = blockIdx.y * A.hc, h1 = min(h0 + A.hc, A.Htot);
-    for (int g = h0; g < h1; g += kAppendAhead) {
-        Unit x[kAppendAhead];
+    auto heads = [&](const T *x, T *y, long long ys, int count, bool turns) {
+        for (int g = 0; g < count; g += kAhead) {
+            Unit v[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAppendAhead; j++) {
-            const int h = g + j, hk = h - A.Hq, hv = hk - P.Hkv;
-            if (h < h1)
-                x[j].load(hk < 0 ? Q + t * A.qs + h * d : hv < 0 ? Kn + t * A.ks + hk * d : Vn + t * A.vs + hv * d, u, d,
-                          A.rot.r, A.nrot);
-        }
+            for (int j = 0; j < kAhead; j++)
+                if (g + j < count) v[j].load(x + j * d, u, d, A.rot.r, A.nrot);
 #pragma unroll
-        for (int j = 0; j < kAppendAhead; j++) {
-            const int h = g + j, hk = h - A.Hq, hv = hk - P.Hkv;
-            if (h >= h1) continue;
-            if (u < A.nrot && hv < 0) x[j].turn(c, s);
-            x[j].store(hk < 0 ? Qo + t * A.qos + h * d : hv < 0 ? Kp + at + hk * P.sh : Vp + at + hv * P.sh, u, d,
-                       A.rot.r, A.nrot);
+            for (int j = 0; j < kAhead; j++) {
+                if (g + j >= count) continue;
+                if (turns) v[j].turn(c, s);
+                v[j].store(y + j * ys, u, d, A.rot.r, A.nrot);
+            }
+            x += kAhead * d;
+            y += kAhead * ys;
         }
+    };
+    const bool turns = u < A.nrot;
+    const int k0 = A.Hq, v0 = k0 + P.Hkv;      // the first of the keys' and of the values' rows
+    if (h0 < k0) heads(Q + t * A.qs + h0 * d, Qo + t * A.qos + h0 * d, d, min(h1, k0) - h0, turns);
+    if (h0 < v0 && h1 > k0) {
+        const int h = max(h0 - k0, 0);
+        heads(Kn + t * A.ks + h * d, Kp + at + h * P.sh, P.sh, min(h1, v0) - k0 - h, turns);
+    }
+    if (h1 > v0) {
+        const int h = max(h0 - v0, 0);
+        heads(Vn + t * A.vs + h * d, Vp + at + h * P.sh, P.sh, h1 - v0 - h, false);
     }
 }
 
@@ -126,7 +136,7 @@ cudaError_t launch_as(AppendArgs &A, const void *Q, void *Qo, const void *Kn, co
     const int per = kAppendThreads / A.units;
     // rows per thread: as many as leave two threads for every one that the GPU holds at once
     // (148 x 2048), else one each, for latency
-    A.hc = 16;
+    A.hc = 32;
     while (A.hc > 1 && (long long)A.T * A.units * ((A.Htot + A.hc - 1) / A.hc) < 2ll * 148 * 2048) A.hc >>= 1;
     LaunchScope scope(kPagedAppend, st);
     return launch_pdl(append_kernel<T, VE, HALF>, dim3((unsigned)((A.T + per - 1) / per), (A.Htot + A.hc - 1) / A.hc),

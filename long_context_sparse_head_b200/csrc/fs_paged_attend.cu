@@ -12,7 +12,8 @@
 // wave takes an equal share of them, found on the device from lens: ragged batches are spread
 // evenly, and the launch does not depend on lens, so a captured graph serves every step.  A row
 // that crosses CTAs is joined by the last of them to arrive, in the order of the CTAs, so the
-// result does not depend on who that is.
+// result does not depend on who that is.  A row's share counts two tiles more than it has: what
+// beginning and ending it costs, without which CTAs with many short rows finish last.
 //
 // Within a CTA each of four warps streams chunks of its own through a ring of three stages
 // (cp.async, 16 bytes a lane, the rows found through the page table one stage ahead) and keeps
@@ -30,6 +31,8 @@
 namespace fs {
 namespace {
 
+constexpr int kSms = 148, kMaxGrid = 2 * kSms;   // two CTAs per SM at most
+constexpr int kFlatJoin = 16;                   // results that one CTA joins at once
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 3;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -107,12 +110,14 @@ template <typename T, int D, int HT> struct Shape {
     static constexpr int kRowBytes = D * (int)sizeof(T);
     static constexpr int kChunkBytes = 2 * kKeys * kRowBytes;                      // K and V
     static constexpr int kWarpBytes = kStages * kChunkBytes;
-    static constexpr int kOutRow = D + 4;                                          // floats; spreads the banks
     static constexpr int kSmem = kWarps * kWarpBytes;
     static constexpr int kPart = HT * D + (HT == 1 ? 4 : 2 * HT);                   // floats of a partial result
     static constexpr int kBlocks = kSmem > 110 * 1024 ? 1 : 2;                     // CTAs per SM
     static_assert(kPart % 4 == 0 && kPart <= 16 * (D + 2), "16-byte vectors, attend_area_bytes");
-    static_assert(HT * kOutRow * 4 <= kWarpBytes, "a warp's result fits in its stages");
+    static_assert(HT * D * 4 <= kChunkBytes, "a warp's result fits in a stage");
+    // place of element d of head h in a warp's result: the four head pairs that a warp writes at
+    // once go to different banks
+    __device__ __forceinline__ static int out(int h, int d) { return h * D + (d ^ (((h >> 1) & 3) << 3)); }
 };
 
 // Where a warp's chunk rows are: lane j < kKeys finds row j, one stage ahead of its use.
@@ -259,7 +264,7 @@ template <typename T, int D, int HT> struct TcState {
             }
         }
     }
-    // m, l and the accumulators to shared memory: out[head][D + 4]
+    // m, l and the accumulators to shared memory
     __device__ __forceinline__ void finish(float *out, float *sm, float *sl, int lane) {
         using S = Shape<T, D, HT>;
 #pragma unroll
@@ -277,8 +282,8 @@ template <typename T, int D, int HT> struct TcState {
                 }
 #pragma unroll
                 for (int t = 0; t < DT; t++) {
-                    out[h * S::kOutRow + 16 * t + lane / 4] = o[t][n][e];
-                    out[h * S::kOutRow + 16 * t + lane / 4 + 8] = o[t][n][e + 2];
+                    out[S::out(h, 16 * t + lane / 4)] = o[t][n][e];
+                    out[S::out(h, 16 * t + lane / 4 + 8)] = o[t][n][e + 2];
                 }
             }
     }
@@ -377,7 +382,7 @@ template <int D, int HT> struct F32State {
                 sl[h] = x;
             }
 #pragma unroll
-            for (int e = 0; e < kOwn; e++) out[h * S::kOutRow + own(lane, e)] = o[h][e];
+            for (int e = 0; e < kOwn; e++) out[S::out(h, own(lane, e))] = o[h][e];
         }
     }
 };
@@ -393,43 +398,89 @@ __device__ __forceinline__ void add4(float4 &a, float f, const float4 &b) {
     a.x = fmaf(f, b.x, a.x); a.y = fmaf(f, b.y, a.y); a.z = fmaf(f, b.z, a.z); a.w = fmaf(f, b.w, a.w);
 }
 
+// Tokens [first, n) that sequence b attends to.
+__device__ __forceinline__ void span(const AttendArgs &A, int b, int &first, int &n) {
+    n = __ldg(A.lens + b);
+    if (n < 0 || n > A.P.cap) {
+        raise_check(A.flag);
+        n = n < 0 ? 0 : A.P.cap;
+    }
+    first = A.window >= 0 ? max(0, n - 1 - A.window) : 0;
+}
+// A row's work in units of a tile's time: what beginning and ending it costs, then its tiles.  An
+// empty sequence has one tile, which writes its zeros.
+constexpr int kRowCost = 2;
+template <int TILE> __device__ __forceinline__ int units_of(int first, int n) {
+    return kRowCost + max(1, (n - first + TILE - 1) / TILE);
+}
+
+// A place in the CTA's share: `left` units from unit `unit` of row r of sequence b.
+struct Place {
+    int b, r, unit, left;
+};
+// One row's part of the share.
+struct Segment {
+    int b, r, unit, unit1, units;              // units [unit, unit1) of the row's
+    int tile, tile1;                           // its tiles
+    int t0, t1, hkv;                           // its tokens [t0, t1)
+    __device__ __forceinline__ bool whole() const { return tile == 0 && unit1 == units; }
+};
+template <int TILE> __device__ __forceinline__ Segment open(const AttendArgs &A, int HG, Place &p) {
+    Segment s;
+    int first, n;
+    span(A, p.b, first, n);
+    s.b = p.b;
+    s.r = p.r;
+    s.unit = p.unit;
+    s.units = units_of<TILE>(first, n);
+    s.unit1 = min(s.units, p.unit + p.left);
+    s.tile = max(0, s.unit - kRowCost);
+    s.tile1 = max(0, s.unit1 - kRowCost);
+    s.t0 = min(n, first + s.tile * TILE);
+    s.t1 = min(n, first + s.tile1 * TILE);
+    s.hkv = A.NG == 1 ? p.r : p.r / A.NG;
+    p.left -= s.unit1 - s.unit;
+    p.unit = s.unit1;
+    if (p.unit == s.units) {
+        p.unit = 0;
+        if (++p.r == HG) {
+            p.r = 0;
+            p.b++;
+        }
+    }
+    return s;
+}
+// Warp w's chunks of a segment: the w-th of every kWarps.
+template <int KEYS> __device__ __forceinline__ int chunks_of(const Segment &s, int warp) {
+    const int chunks = max(0, (s.t1 - s.t0 + KEYS - 1) / KEYS);
+    return (chunks - warp + kWarps - 1) / kWarps;
+}
+
 template <typename T, int D, int HT>
 __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
     paged_attend_kernel(const __grid_constant__ AttendArgs A, const T *__restrict__ Q, const T *__restrict__ Kp,
                         const T *__restrict__ Vp, T *__restrict__ O, float *__restrict__ lse) {
     using S = Shape<T, D, HT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_m[kWarps][HT], s_l[kWarps][HT], s_f[HT];
+    __shared__ float s_m[kWarps][HT], s_l[kWarps][HT], s_fac[HT][33];
     __shared__ __align__(16) float s_q[S::kTc ? 1 : HT * D];
     __shared__ float s_p[S::kTc ? 1 : kWarps * S::kKeys * HT];
     __shared__ long long s_sum[kWarps], s_rem;
-    __shared__ int s_b, s_last;
+    __shared__ int s_b, s_last, s_out[kWarps];
     const PagedDev &P = A.P;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int HG = P.Hkv * A.NG;
     griddep_wait();
 
-    // tokens that sequence b attends to: [first, len); an empty one has a tile of its own, which
-    // writes its zeros
-    auto span = [&](int b, int &first) {
-        int n = __ldg(A.lens + b);
-        if (n < 0 || n > P.cap) {
-            raise_check(A.flag);
-            n = n < 0 ? 0 : P.cap;
-        }
-        first = A.window >= 0 ? max(0, n - 1 - A.window) : 0;
-        return n;
+    // this CTA's share of all rows' units, and where it begins
+    auto units_at = [&](int b) {
+        int first, n;
+        span(A, b, first, n);
+        return units_of<S::kTile>(first, n);
     };
-    auto tiles_of = [&](int b) {
-        int first;
-        const int n = span(b, first);
-        return max(1, (n - first + S::kTile - 1) / S::kTile);
-    };
-
-    // this CTA's share [at, end) of all rows' tiles, and the sequence it begins in
     const int seg = (P.B + kThreads - 1) / kThreads, b0 = min(P.B, tid * seg), b1 = min(P.B, b0 + seg);
     long long mine = 0;
-    for (int b = b0; b < b1; b++) mine += tiles_of(b);
+    for (int b = b0; b < b1; b++) mine += units_at(b);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -452,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
         long long x = (before + incl - mine) * HG;
         if (begin >= x && begin < x + mine * HG)
             for (int b = b0; b < b1; b++) {
-                const long long n = (long long)tiles_of(b) * HG;
+                const long long n = (long long)units_at(b) * HG;
                 if (begin < x + n) {
                     s_b = b;
                     s_rem = begin - x;
@@ -462,56 +513,77 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
             }
     }
     __syncthreads();
-    int b = s_b;
-    long long rem = s_rem, at = begin;         // tiles into sequence b, tiles into all
+    Place at;
+    at.b = s_b;
+    {
+        const int units = units_at(at.b);
+        at.r = (int)(s_rem / units);
+        at.unit = (int)(s_rem - (long long)at.r * units);
+        at.left = (int)(end - begin);          // <= 2^31 for any batch that fits a GPU's memory
+    }
 
+    // The warp's ring of stages runs on over the rows: `ahead` is the segment whose chunks are
+    // being fetched, `next` of its `chunks` chunks are; `rows` has found the one to fetch next.
     uint8_t *wsm = smem + warp * S::kWarpBytes;
     const uint32_t wst = smem_addr(wsm);
-    while (at < end) {
-        int first;
-        const int n = span(b, first);
-        const int tiles = max(1, (n - first + S::kTile - 1) / S::kTile);
-        const int r = (int)(rem / tiles), tile = (int)(rem - (long long)r * tiles);
-        const int tile1 = (int)min((long long)tiles, tile + (end - at));
-        const int hkv = r / A.NG, h0 = hkv * A.G + (r - hkv * A.NG) * HT;      // first query head
-        const int heads = min(HT, (hkv + 1) * A.G - h0);
-        const int t0 = first + tile * S::kTile, t1 = min(n, first + tile1 * S::kTile);
-        const int chunks = max(0, (t1 - t0 + S::kKeys - 1) / S::kKeys);
-        const int cnt = (chunks - warp + kWarps - 1) / kWarps;                 // this warp's
-        const int32_t *trow = A.table + (long long)b * P.max_pages;
-        const T *Kh = Kp + hkv * P.sh, *Vh = Vp + hkv * P.sh;
-        const T *Qr = Q + b * A.qs + h0 * D;
-
-        auto tok0 = [&](int i) { return t0 + (warp + kWarps * i) * S::kKeys; };
-        Rows<S::kKeys> rows;
-        rows.find(P, trow, tok0(0), t1, lane);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; i++) {
-            if (i < cnt) fetch<T, D, HT>(rows, A, Kh, Vh, wst + i * S::kChunkBytes, lane);
-            cp_commit();
-            if (i + 1 < cnt) rows.find(P, trow, tok0(i + 1), t1, lane);
+    Place fat = at;
+    Segment ahead;
+    int chunks = 0, next = 0;
+    bool more = true;
+    Rows<S::kKeys> rows;
+    auto find = [&]() {
+        while (next >= chunks) {
+            if (fat.left <= 0) {
+                more = false;
+                return;
+            }
+            ahead = open<S::kTile>(A, HG, fat);
+            chunks = chunks_of<S::kKeys>(ahead, warp);
+            next = 0;
+            // its query rows, to L2: they are read when the row is begun
+            const int h0 = ahead.hkv * A.G + (ahead.r - ahead.hkv * A.NG) * HT;
+            if (warp == 0 && lane * (128 / (int)sizeof(T)) < min(HT, (ahead.hkv + 1) * A.G - h0) * D)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(Q + ahead.b * A.qs + h0 * D + lane * (128 / (int)sizeof(T))));
         }
-        float *out = reinterpret_cast<float *>(wsm);
+        rows.find(P, A.table + (long long)ahead.b * P.max_pages, ahead.t0 + (warp + kWarps * next) * S::kKeys, ahead.t1, lane);
+        next++;
+    };
+    auto fill = [&](int slot) {
+        if (more) {
+            fetch<T, D, HT>(rows, A, Kp + ahead.hkv * P.sh, Vp + ahead.hkv * P.sh, wst + slot * S::kChunkBytes, lane);
+            find();
+        }
+        cp_commit();
+    };
+    find();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; i++) fill(i);
+
+    int slot = 0, free = kStages - 1;          // the stage to work on, the one that is free
+    long long done = begin;
+    while (at.left > 0) {
+        const Segment g = open<S::kTile>(A, HG, at);
+        if (g.tile1 == 0) break;               // the row's beginning alone, at the end of the share
+        const int h0 = g.hkv * A.G + (g.r - g.hkv * A.NG) * HT;                // first query head
+        const int heads = min(HT, (g.hkv + 1) * A.G - h0);
+        const T *Qr = Q + g.b * A.qs + h0 * D;
+        const int cnt = chunks_of<S::kKeys>(g, warp);
         auto stream = [&](auto &&work) {
-            int slot = 0, fill = kStages - 1;
             for (int i = 0; i < cnt; i++) {
                 cp_wait<kStages - 2>();
                 __syncwarp();
-                if (i + kStages - 1 < cnt) fetch<T, D, HT>(rows, A, Kh, Vh, wst + fill * S::kChunkBytes, lane);
-                cp_commit();
-                if (i + kStages < cnt) rows.find(P, trow, tok0(i + kStages), t1, lane);
-                work(slot * S::kChunkBytes, min(S::kKeys, t1 - tok0(i)));
+                fill(free);
+                work(slot * S::kChunkBytes, min(S::kKeys, g.t1 - g.t0 - (warp + kWarps * i) * S::kKeys));
+                free = slot;
                 slot = slot + 1 == kStages ? 0 : slot + 1;
-                fill = fill + 1 == kStages ? 0 : fill + 1;
             }
-            cp_wait<0>();
-            __syncwarp();                      // the stages are free for the result
+            __syncwarp();                      // the free stage takes the result
         };
         if constexpr (S::kTc) {
             TcState<T, D, HT> st;
             st.start(Qr, heads, lane);
             stream([&](int off, int left) { st.chunk(wst + off, left, A.scale2, lane); });
-            st.finish(out, s_m[warp], s_l[warp], lane);
+            st.finish(reinterpret_cast<float *>(wsm + free * S::kChunkBytes), s_m[warp], s_l[warp], lane);
         } else {
             for (int x = tid; x < HT * D; x += kThreads) s_q[x] = x / D < heads ? (float)Qr[x] : 0.f;
             __syncthreads();
@@ -520,14 +592,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
             stream([&](int off, int left) {
                 st.chunk(wsm + off, s_q, s_p + warp * S::kKeys * HT, left, A.scale2, lane);
             });
-            st.finish(out, s_m[warp], s_l[warp], lane);
+            st.finish(reinterpret_cast<float *>(wsm + free * S::kChunkBytes), s_m[warp], s_l[warp], lane);
         }
+        if (lane == 0) s_out[warp] = warp * S::kWarpBytes + free * S::kChunkBytes;
         __syncthreads();
 
         // the four warps' results joined
-        const bool whole = tile == 0 && tile1 == tiles;
-        const long long row0 = at - tile;                                      // the row's first tile among all
-        float *part = A.part + ((long long)blockIdx.x * 2 + (tile == 0)) * S::kPart;
+        const bool whole = g.whole();
+        float *part = A.part + ((long long)blockIdx.x * 2 + (g.tile == 0)) * S::kPart;
         for (int x = tid; x < heads * (D / 4); x += kThreads) {
             const int h = x / (D / 4), c = x % (D / 4) * 4;
             float m = s_m[0][h], l = 0.f;
@@ -539,11 +611,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
             for (int w = 0; w < kWarps; w++) {
                 const float f = exp2f(s_m[w][h] - ref);
                 l = fmaf(f, s_l[w][h], l);
-                add4(o, f, *reinterpret_cast<const float4 *>(smem + w * S::kWarpBytes + (h * S::kOutRow + c) * 4));
+                add4(o, f, *reinterpret_cast<const float4 *>(smem + s_out[w] + S::out(h, c) * 4));
             }
             if (whole) {
-                store4(O + b * A.os + (h0 + h) * D + c, o, l == 0.f ? 0.f : 1.f / l);
-                if (lse && c == 0) lse[(long long)b * P.H + h0 + h] = (m + log2f(l)) * kLn2;
+                store4(O + g.b * A.os + (h0 + h) * D + c, o, l == 0.f ? 0.f : 1.f / l);
+                if (lse && c == 0) lse[(long long)g.b * P.H + h0 + h] = (m + log2f(l)) * kLn2;
             } else {
                 *reinterpret_cast<float4 *>(part + h * D + c) = o;
                 if (c == 0) {
@@ -553,56 +625,103 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
             }
         }
         if (!whole) {
-            const int c0 = (int)(row0 / per), c1 = (int)((row0 + tiles - 1) / per);   // the CTAs of the row
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(A.count + c0, 1) == c1 - c0;
-            __syncthreads();
-            if (s_last) {
+            const long long row0 = done - g.unit;                              // the row's first unit among all
+            const int c0 = (int)((row0 + kRowCost) / per), n = (int)((row0 + g.units - 1) / per) - c0 + 1;   // its CTAs
+            // c0's result of the row is its second (the row begins there), the others' their first
+            auto part_of = [&](int i) { return A.part + ((long long)(c0 + i) * 2 + (i == 0)) * S::kPart; };
+            // whether this CTA is the last of `count` to arrive
+            auto last = [&](int *counter, int count) {
                 __threadfence();
-                // c0 holds the row's beginning (its second part), the others continue it (their first)
-                auto at_part = [&](int i) { return A.part + ((long long)(c0 + i) * 2 + (i == 0)) * S::kPart; };
-                const int np = c1 - c0 + 1;
-                for (int h = warp; h < heads; h += kWarps) {
-                    float m = -INFINITY, l = 0.f;
-                    for (int i = lane; i < np; i += 32) m = fmaxf(m, __ldcg(at_part(i) + HT * D + h));
-                    m = warp_max(m);
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    for (int i = lane; i < np; i += 32)
-                        l = fmaf(exp2f(__ldcg(at_part(i) + HT * D + h) - ref), __ldcg(at_part(i) + HT * D + HT + h), l);
-                    l = warp_sum(l);
-                    if (lane == 0) {
-                        s_m[0][h] = ref;
-                        s_f[h] = l == 0.f ? 0.f : 1.f / l;
-                        if (lse) lse[(long long)b * P.H + h0 + h] = (m + log2f(l)) * kLn2;
+                __syncthreads();
+                if (tid == 0) {
+                    s_last = atomicAdd(counter, 1) == count - 1;
+                    if (s_last) *counter = 0;                                  // for the next call
+                }
+                __syncthreads();
+                if (s_last) __threadfence();
+                return s_last != 0;
+            };
+            // the results i0, i0 + step, ... (count <= 32 of them) joined: to `to`, or as the row's output
+            auto join = [&](int i0, int step, int count, float *to) {
+                constexpr int kOwn = (HT + kWarps - 1) / kWarps;
+                float m[kOwn], l[kOwn];
+#pragma unroll
+                for (int k = 0; k < kOwn; k++) {
+                    const int h = warp + kWarps * k;
+                    const bool in = h < heads && lane < count;
+                    const float *p = part_of(i0 + (in ? lane : 0) * step) + HT * D;
+                    m[k] = in ? __ldcg(p + h) : -INFINITY;
+                    l[k] = in ? __ldcg(p + HT + h) : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < kOwn; k++) {
+                    const int h = warp + kWarps * k;
+                    const float top = warp_max(m[k]), f = exp2f(m[k] - (top == -INFINITY ? 0.f : top));
+                    const float sum = warp_sum(f * l[k]);
+                    if (h < heads) {
+                        s_fac[h][lane] = f;
+                        if (lane == 0) {
+                            s_m[0][h] = top;
+                            s_l[0][h] = sum;
+                        }
                     }
                 }
                 __syncthreads();
-                for (int x = tid; x < heads * (D / 4); x += kThreads) {
-                    const int h = x / (D / 4), c = x % (D / 4) * 4;
-                    const float ref = s_m[0][h];
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int items = heads * (D / 4);
+                for (int x = tid; x < items; x += 2 * kThreads) {              // two float4 a thread at once
+                    const int y = x + kThreads < items ? x + kThreads : x;
+                    const int hx = x / (D / 4), hy = y / (D / 4);
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
 #pragma unroll 8
-                    for (int i = 0; i < np; i++) {
-                        const float *p = at_part(i);
-                        add4(o, exp2f(__ldcg(p + HT * D + h) - ref), __ldcg(reinterpret_cast<const float4 *>(p + h * D + c)));
+                    for (int i = 0; i < count; i++) {
+                        const float4 *p = reinterpret_cast<const float4 *>(part_of(i0 + i * step));
+                        add4(a, s_fac[hx][i], __ldcg(p + x));
+                        add4(b, s_fac[hy][i], __ldcg(p + y));
                     }
-                    store4(O + b * A.os + (h0 + h) * D + c, o, s_f[h]);
+                    auto put = [&](int z, int h, const float4 &v) {
+                        const int c = z % (D / 4) * 4;
+                        const float l = s_l[0][h];
+                        if (to) {
+                            reinterpret_cast<float4 *>(to)[z] = v;
+                            if (c == 0) {
+                                to[HT * D + h] = s_m[0][h];
+                                to[HT * D + HT + h] = l;
+                            }
+                        } else {
+                            store4(O + g.b * A.os + (h0 + h) * D + c, v, l == 0.f ? 0.f : 1.f / l);
+                            if (lse && c == 0) lse[(long long)g.b * P.H + h0 + h] = (s_m[0][h] + log2f(l)) * kLn2;
+                        }
+                    };
+                    put(x, hx, a);
+                    if (y != x) put(y, hy, b);
                 }
-                if (tid == 0) A.count[c0] = 0;                                 // for the next call
+            };
+            // A row over many CTAs is joined in two steps, groups of about sqrt(n) side by side and
+            // then their results: one CTA reads n results no faster than one after the other.
+            // Counters: of a group by its first CTA, of rows that begin there and of rows that
+            // go on there apart; of the groups by the row's first CTA.
+            if (n <= kFlatJoin) {
+                if (last(A.count + c0, n)) join(0, 1, n, nullptr);
+            } else {
+                int size = kFlatJoin / 2;
+                while (size * size < n) size++;
+                const int first = ((int)blockIdx.x - c0) / size * size;        // of the CTA's group
+                const int count = min(size, n - first);
+                if (last(A.count + (first ? kMaxGrid : 0) + c0 + first, count)) {
+                    join(first, 1, count, part_of(first));
+                    const int groups = (n + size - 1) / size;
+                    if (last(A.count + 2 * kMaxGrid + c0, groups)) {
+                        __syncthreads();
+                        join(0, size, groups, nullptr);
+                    }
+                }
             }
         }
-        __syncthreads();                       // the stages, s_m and s_l are free again
-        at += tile1 - tile;
-        rem += tile1 - tile;
-        if (rem == (long long)tiles * HG) {
-            rem = 0;
-            b++;
-        }
+        __syncthreads();                       // the results, s_m and s_l are free again
+        done += g.unit1 - g.unit;
     }
 }
 
-constexpr int kSms = 148;
 
 template <typename T, int D, int HT>
 cudaError_t launch_as(AttendArgs &A, const void *Q, const void *Kp, const void *Vp, void *O, float *lse,
@@ -616,7 +735,7 @@ cudaError_t launch_as(AttendArgs &A, const void *Q, const void *Kp, const void *
     const long long most = (long long)A.P.B * A.P.Hkv * A.NG *
                            (((A.window >= 0 && A.window < A.P.cap ? A.window + 1 : A.P.cap) + S::kTile - 1) / S::kTile);
     const int grid = (int)(most < kSms * S::kBlocks ? (most < 1 ? 1 : most) : kSms * S::kBlocks);
-    static_assert(kSms * 2 <= kPagedMaxCtas, "a counter for every CTA");
+    static_assert(3 * kMaxGrid <= kPagedCounts, "three counters for every CTA");
     LaunchScope scope(kPagedAttend, st);
     return launch_pdl(kern, dim3(grid), dim3(kThreads), S::kSmem, st, A, (const T *)Q, (const T *)Kp, (const T *)Vp,
                       (T *)O, lse);
@@ -657,7 +776,7 @@ cudaError_t launch_attend(AttendArgs &A, const void *Q, const void *Kp, const vo
 }  // namespace
 
 // two partial results for every CTA, of at most 16 heads
-size_t attend_area_bytes(const fs_paged_params *p) { return (size_t)kSms * 2 * 2 * 16 * (p->d + 2) * 4; }
+size_t attend_area_bytes(const fs_paged_params *p) { return (size_t)kMaxGrid * 2 * 16 * (p->d + 2) * 4; }
 
 }  // namespace fs
 

@@ -28,12 +28,12 @@ struct RopeArgs {
 };
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeAhead = 4;                  // heads in flight per thread
 
 template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs A,
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_constant__ RopeArgs A,
                                                             const T *Q, T *Qo, const T *K, T *Ko) {
     using Unit = RowUnit<T, VE, HALF>;
+    constexpr int kRopeAhead = HALF ? 2 : 4;   // heads in flight per thread: four vectors either way
     griddep_wait();
     const int per = kRopeThreads / A.units;    // tokens per block
     const int lt = threadIdx.x / A.units, u = threadIdx.x - lt * A.units;
@@ -47,24 +47,31 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         for (int m = 0; m < Unit::kPairs; m++)
             rotary_angle(A.rot.turns[Unit::pair(u, m)], pos, A.rot.mscale, A.sign, c[m], s[m]);
     }
+    // this block's heads: some of Q's, then some of K's
     const int h0 = blockIdx.y * A.hc, h1 = min(h0 + A.hc, A.Htot);
-    const long long qi = b * A.qs[0] + n * A.qs[2], qo = b * A.qos[0] + n * A.qos[2];
-    const long long ki = b * A.ks[0] + n * A.ks[2], ko = b * A.kos[0] + n * A.kos[2];
-    for (int g = h0; g < h1; g += kRopeAhead) {
-        Unit x[kRopeAhead];
+    auto heads = [&](const T *x, T *y, long long xs, long long ys, int count) {
+        for (int g = 0; g < count; g += kRopeAhead) {
+            Unit v[kRopeAhead];
 #pragma unroll
-        for (int j = 0; j < kRopeAhead; j++) {
-            const int h = g + j;
-            if (h < h1)
-                x[j].load(h < A.H ? Q + qi + h * A.qs[1] : K + ki + (h - A.H) * A.ks[1], u, A.d, A.rot.r, A.nrot);
-        }
+            for (int j = 0; j < kRopeAhead; j++)
+                if (g + j < count) v[j].load(x + j * xs, u, A.d, A.rot.r, A.nrot);
 #pragma unroll
-        for (int j = 0; j < kRopeAhead; j++) {
-            const int h = g + j;
-            if (h >= h1) continue;
-            if (u < A.nrot) x[j].turn(c, s);
-            x[j].store(h < A.H ? Qo + qo + h * A.qos[1] : Ko + ko + (h - A.H) * A.kos[1], u, A.d, A.rot.r, A.nrot);
+            for (int j = 0; j < kRopeAhead; j++) {
+                if (g + j >= count) continue;
+                if (u < A.nrot) v[j].turn(c, s);
+                v[j].store(y + j * ys, u, A.d, A.rot.r, A.nrot);
+            }
+            x += kRopeAhead * xs;
+            y += kRopeAhead * ys;
         }
+    };
+    if (h0 < A.H)
+        heads(Q + b * A.qs[0] + n * A.qs[2] + h0 * A.qs[1], Qo + b * A.qos[0] + n * A.qos[2] + h0 * A.qos[1], A.qs[1],
+              A.qos[1], min(h1, A.H) - h0);
+    if (h1 > A.H) {
+        const int k0 = max(h0 - A.H, 0);
+        heads(K + b * A.ks[0] + n * A.ks[2] + k0 * A.ks[1], Ko + b * A.kos[0] + n * A.kos[2] + k0 * A.kos[1], A.ks[1],
+              A.kos[1], h1 - A.H - k0);
     }
 }
 
@@ -77,7 +84,7 @@ cudaError_t launch_as(RopeArgs &A, bool in_place, const void *Q, void *Qo, const
     const unsigned gx = (unsigned)((A.T + per - 1) / per);
     // heads per thread: as many as leave two threads for every one that the GPU holds at once
     // (148 x 2048), else a head each, for latency
-    A.hc = 16;
+    A.hc = 32;
     while (A.hc > 1 && (long long)A.T * A.units * ((A.Htot + A.hc - 1) / A.hc) < 2ll * 148 * 2048) A.hc >>= 1;
     if (A.hc < A.Htot && (A.Htot + A.hc - 1) / A.hc > 65535) return cudaErrorInvalidValue;
     LaunchScope scope(kRope, st);

@@ -40,6 +40,27 @@ __device__ __forceinline__ void rotary_angle(unsigned long long turns, long long
     s = b * (mscale * sign);
 }
 
+// Two 16-bit elements of a 32-bit word, widened and rounded together.
+template <typename T> struct Two;
+template <> struct Two<__nv_bfloat16> {
+    __device__ __forceinline__ static float2 get(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ static uint32_t put(float a, float b) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+};
+template <> struct Two<__half> {
+    __device__ __forceinline__ static float2 get(uint32_t w) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    __device__ __forceinline__ static uint32_t put(float a, float b) {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+};
+
 // N elements in one access of N * sizeof(T) bytes (N = 1: one element).
 template <typename T, int N> struct alignas(N * sizeof(T)) Pack {
     T e[N];
@@ -86,14 +107,34 @@ template <typename T, int VE, bool HALF> struct RowUnit {
     }
     // the pairs turned in fp32 and rounded once to T
     __device__ __forceinline__ void turn(const float (&c)[kPairs], const float (&s)[kPairs]) {
+        if constexpr (sizeof(T) == 2 && VE > 1) {              // word by word: one instruction rounds two
+            uint32_t *x = reinterpret_cast<uint32_t *>(&v[0]);
+            if constexpr (HALF) {
+                uint32_t *y = reinterpret_cast<uint32_t *>(&v[1]);
 #pragma unroll
-        for (int m = 0; m < kPairs; m++) {
-            constexpr bool split = VE == 1 || HALF;          // the pair's elements are in two accesses
-            T &x = split ? v[0].e[VE == 1 ? 0 : m] : v[0].e[VE == 1 ? 0 : 2 * m];
-            T &y = split ? v[kVecs - 1].e[VE == 1 ? 0 : m] : v[0].e[VE == 1 ? 0 : 2 * m + 1];
-            const float a = to_f<T>(x), b = to_f<T>(y);
-            x = from_f<T>(fmaf(a, c[m], -b * s[m]));
-            y = from_f<T>(fmaf(a, s[m], b * c[m]));
+                for (int w = 0; w < VE / 2; w++) {
+                    const float2 a = Two<T>::get(x[w]), b = Two<T>::get(y[w]);
+                    const int m = 2 * w;
+                    x[w] = Two<T>::put(fmaf(a.x, c[m], -b.x * s[m]), fmaf(a.y, c[m + 1], -b.y * s[m + 1]));
+                    y[w] = Two<T>::put(fmaf(a.x, s[m], b.x * c[m]), fmaf(a.y, s[m + 1], b.y * c[m + 1]));
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < VE / 2; m++) {
+                    const float2 a = Two<T>::get(x[m]);
+                    x[m] = Two<T>::put(fmaf(a.x, c[m], -a.y * s[m]), fmaf(a.x, s[m], a.y * c[m]));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < kPairs; m++) {
+                constexpr bool split = VE == 1 || HALF;        // the pair's elements are in two accesses
+                T &x = split ? v[0].e[VE == 1 ? 0 : m] : v[0].e[VE == 1 ? 0 : 2 * m];
+                T &y = split ? v[kVecs - 1].e[VE == 1 ? 0 : m] : v[0].e[VE == 1 ? 0 : 2 * m + 1];
+                const float a = to_f<T>(x), b = to_f<T>(y);
+                x = from_f<T>(fmaf(a, c[m], -b * s[m]));
+                y = from_f<T>(fmaf(a, s[m], b * c[m]));
+            }
         }
     }
     // index of pair m of a turning unit

@@ -124,7 +124,8 @@ def rope(rot, **kw):
     c = fs.FsRopeParams(2, 8, 4, 2, 64)
     for name in ("q", "qo", "k", "ko"):
         heads = 4 if name[0] == "q" else 2
-        getattr(c, name)[:] = kw.pop(name + "_strides", (heads * 8 * 64, 8 * 64, 64))
+        for x, v in zip("bhn", kw.pop(name + "_strides", (heads * 8 * 64, 8 * 64, 64))):
+            setattr(c, name + "_" + x, v)
     c.dtype = kw.pop("dtype", 0)
     a = dict(Q=PTR, Qo=PTR + 65536, K=PTR, Ko=PTR + 65536)
     for n in ("B", "N", "H", "Hk", "d"):
