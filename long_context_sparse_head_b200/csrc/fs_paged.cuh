@@ -38,7 +38,7 @@ struct PagedDev {
 // calls for their lists.  Flag and counters lie at the same place whatever the parameters, so
 // a workspace made for the largest batch serves smaller ones.
 constexpr size_t kPagedCounters = 256;
-constexpr int kPagedCounts = 1024;
+constexpr int kPagedCounts = 1536;
 constexpr size_t kPagedArea = kPagedCounters + 4 * (size_t)kPagedCounts;
 
 size_t attend_area_bytes(const fs_paged_params *p);

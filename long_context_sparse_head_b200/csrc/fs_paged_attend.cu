@@ -12,10 +12,10 @@
 // wave takes an equal share of them, found on the device from lens: ragged batches are spread
 // evenly, and the launch does not depend on lens, so a captured graph serves every step.  A row
 // that crosses CTAs is joined by the last of them to arrive, in the order of the CTAs, so the
-// result does not depend on who that is.  A row's share counts two tiles more than it has: what
+// result does not depend on who that is.  A row counts two tiles more than it has: what
 // beginning and ending it costs, without which CTAs with many short rows finish last.
 //
-// Within a CTA each of four warps streams chunks of its own through a ring of three stages
+// Within a CTA each of four warps streams chunks of its own through a ring of two or three stages
 // (cp.async, 16 bytes a lane, the rows found through the page table one stage ahead) and keeps
 // its own m, sum and accumulators: no barrier until the row ends.
 //
@@ -31,9 +31,9 @@
 namespace fs {
 namespace {
 
-constexpr int kSms = 148, kMaxGrid = 2 * kSms;   // two CTAs per SM at most
+constexpr int kSms = 148, kMaxGrid = 3 * kSms;   // three CTAs per SM at most
 constexpr int kFlatJoin = 16;                   // results that one CTA joins at once
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 3;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct AttendArgs {
@@ -109,10 +109,13 @@ template <typename T, int D, int HT> struct Shape {
     static constexpr int kTile = kWarps * kKeys;                                   // tokens of a tile
     static constexpr int kRowBytes = D * (int)sizeof(T);
     static constexpr int kChunkBytes = 2 * kKeys * kRowBytes;                      // K and V
+    // Stages of a warp's ring and CTAs per SM: three CTAs of two stages where their registers fit
+    // (168 a thread), which hide one another's row ends; else two, or one where a chunk is 16 KB.
+    static constexpr int kBlocks = D == 256 ? 1 : HT <= (kTc ? 8 : 4) ? 3 : 2;
+    static constexpr int kStages = kBlocks == 3 ? 2 : 3;
     static constexpr int kWarpBytes = kStages * kChunkBytes;
     static constexpr int kSmem = kWarps * kWarpBytes;
     static constexpr int kPart = HT * D + (HT == 1 ? 4 : 2 * HT);                   // floats of a partial result
-    static constexpr int kBlocks = kSmem > 110 * 1024 ? 1 : 2;                     // CTAs per SM
     static_assert(kPart % 4 == 0 && kPart <= 16 * (D + 2), "16-byte vectors, attend_area_bytes");
     static_assert(HT * D * 4 <= kChunkBytes, "a warp's result fits in a stage");
     // place of element d of head h in a warp's result: the four head pairs that a warp writes at
@@ -557,9 +560,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
     };
     find();
 #pragma unroll
-    for (int i = 0; i < kStages - 1; i++) fill(i);
+    for (int i = 0; i < S::kStages - 1; i++) fill(i);
 
-    int slot = 0, free = kStages - 1;          // the stage to work on, the one that is free
+    int slot = 0, free = S::kStages - 1;          // the stage to work on, the one that is free
     long long done = begin;
     while (at.left > 0) {
         const Segment g = open<S::kTile>(A, HG, at);
@@ -570,12 +573,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
         const int cnt = chunks_of<S::kKeys>(g, warp);
         auto stream = [&](auto &&work) {
             for (int i = 0; i < cnt; i++) {
-                cp_wait<kStages - 2>();
+                cp_wait<S::kStages - 2>();
                 __syncwarp();
                 fill(free);
                 work(slot * S::kChunkBytes, min(S::kKeys, g.t1 - g.t0 - (warp + kWarps * i) * S::kKeys));
                 free = slot;
-                slot = slot + 1 == kStages ? 0 : slot + 1;
+                slot = slot + 1 == S::kStages ? 0 : slot + 1;
             }
             __syncwarp();                      // the free stage takes the result
         };
@@ -631,14 +634,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
             auto part_of = [&](int i) { return A.part + ((long long)(c0 + i) * 2 + (i == 0)) * S::kPart; };
             // whether this CTA is the last of `count` to arrive
             auto last = [&](int *counter, int count) {
-                __threadfence();
                 __syncthreads();
                 if (tid == 0) {
-                    s_last = atomicAdd(counter, 1) == count - 1;
+                    // releases what the block wrote before the barrier, acquires what those before it did
+                    int before;
+                    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+                    s_last = before == count - 1;
                     if (s_last) *counter = 0;                                  // for the next call
                 }
                 __syncthreads();
-                if (s_last) __threadfence();
                 return s_last != 0;
             };
             // the results i0, i0 + step, ... (count <= 32 of them) joined: to `to`, or as the row's output
