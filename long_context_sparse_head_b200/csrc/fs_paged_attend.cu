@@ -27,6 +27,7 @@
 // win, and its operands could not be read in pages of any size.
 // f32: a lane (or two, or four) per key for the scores, lanes over d for the values, fp32 FMA.
 #include "fs_paged.cuh"
+#include "tc_common.cuh"
 
 namespace fs {
 namespace {
@@ -111,7 +112,7 @@ template <typename T, int D, int HT> struct Shape {
     static constexpr int kChunkBytes = 2 * kKeys * kRowBytes;                      // K and V
     // Stages of a warp's ring and CTAs per SM: three CTAs of two stages where their registers fit
     // (168 a thread), which hide one another's row ends; else two, or one where a chunk is 16 KB.
-    static constexpr int kBlocks = D == 256 ? 1 : HT <= (kTc ? 8 : 4) ? 3 : 2;
+    static constexpr int kBlocks = D == 256 ? 1 : HT <= 8 || D == 64 ? 3 : 2;
     static constexpr int kStages = kBlocks == 3 ? 2 : 3;
     static constexpr int kWarpBytes = kStages * kChunkBytes;
     static constexpr int kSmem = kWarps * kWarpBytes;
@@ -162,21 +163,33 @@ __device__ __forceinline__ void fetch(const Rows<Shape<T, D, HT>::kKeys> &R, con
 
 // A warp's running softmax and accumulators, tensor-core form.  Lane l holds, for heads
 // 8 n + 2 (l % 4) + {0, 1}, the accumulator rows d = 16 t + l / 4 + {0, 8}.
+// The queries are operands held in registers, or, where these and the accumulators would take over
+// 190, read from shared memory for every chunk.
 template <typename T, int D, int HT> struct TcState {
     static constexpr int NT = HT / 8, DT = D / 16, MT = Shape<T, D, HT>::kKeys / 16;
-    uint32_t q[NT][DT][2];
+    static constexpr bool kQShared = HT * D > 2048;
+    uint32_t q[kQShared ? 1 : NT][kQShared ? 1 : DT][2];
     float m[NT][2], l[NT][2], o[DT][NT][4];
 
     // heads past the group's last are zeros and never written out
-    __device__ __forceinline__ void start(const T *Q, int heads, int lane) {
+    __device__ __forceinline__ void start(const T *Q, int heads, uint4 *sq, int lane) {
+        if constexpr (kQShared) {              // 16-byte column c of head h at column c ^ (h & 7)
+            for (int x = threadIdx.x; x < HT * D / 8; x += kThreads) {
+                const int h = x / (D / 8), c = x % (D / 8);
+                sq[h * (D / 8) + (c ^ (h & 7))] = h < heads ? __ldg(reinterpret_cast<const uint4 *>(Q) + x) : make_uint4(0, 0, 0, 0);
+            }
+            __syncthreads();
+        }
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            const int h = 8 * n + lane / 4;
-            const uint32_t *row = reinterpret_cast<const uint32_t *>(Q + h * D);
+            if constexpr (!kQShared) {
+                const int h = 8 * n + lane / 4;
+                const uint32_t *row = reinterpret_cast<const uint32_t *>(Q + h * D);
 #pragma unroll
-            for (int t = 0; t < DT; t++)
+                for (int t = 0; t < DT; t++)
 #pragma unroll
-                for (int e = 0; e < 2; e++) q[n][t][e] = h < heads ? __ldg(row + 8 * t + 4 * e + lane % 4) : 0u;
+                    for (int e = 0; e < 2; e++) q[n][t][e] = h < heads ? __ldg(row + 8 * t + 4 * e + lane % 4) : 0u;
+            }
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
 #pragma unroll
@@ -186,7 +199,7 @@ template <typename T, int D, int HT> struct TcState {
         }
     }
     // `left` keys of the chunk exist
-    __device__ __forceinline__ void chunk(uint32_t stage, int left, float scale2, int lane) {
+    __device__ __forceinline__ void chunk(uint32_t stage, uint32_t sq, int left, float scale2, int lane) {
         using S = Shape<T, D, HT>;
         float s[MT][NT][4];
 #pragma unroll
@@ -198,11 +211,21 @@ template <typename T, int D, int HT> struct TcState {
             const int row = 16 * i + (lane & 15);
             const uint32_t base = stage + row * S::kRowBytes;
 #pragma unroll
-            for (int t = 0; t < DT; t++) {
-                uint32_t a[4];
-                ldsm4(a, base + (((2 * t + (lane >> 4)) ^ (row & 7)) << 4));
+            for (int t = 0; t < DT; t += 2) {
+                uint32_t a[2][4];
+                ldsm4(a[0], base + (((2 * t + (lane >> 4)) ^ (row & 7)) << 4));
+                ldsm4(a[1], base + (((2 * t + 2 + (lane >> 4)) ^ (row & 7)) << 4));
 #pragma unroll
-                for (int n = 0; n < NT; n++) Half2<T>::mma(s[i][n], a, q[n][t][0], q[n][t][1]);
+                for (int n = 0; n < NT; n++) {
+                    uint32_t b[4];
+                    if constexpr (kQShared) {
+                        ldsm4(b, sq + (8 * n + (lane & 7)) * D * 2 + (((2 * t + (lane >> 3)) ^ (lane & 7)) << 4));
+                    } else {
+                        b[0] = q[n][t][0]; b[1] = q[n][t][1]; b[2] = q[n][t + 1][0]; b[3] = q[n][t + 1][1];
+                    }
+                    Half2<T>::mma(s[i][n], a[0], b[0], b[1]);
+                    Half2<T>::mma(s[i][n], a[1], b[2], b[3]);
+                }
             }
         }
         bool up = false;
@@ -292,101 +315,202 @@ template <typename T, int D, int HT> struct TcState {
     }
 };
 
-// The same in fp32 FMA.  Scores: lane l takes key l % KEYS and every kParts-th 16-byte column
-// from l / KEYS on.  Values: lane l holds the d's of its 16-byte (D = 64: 8-byte) columns.
+// The same in fp32, two multiply-adds an instruction.  Scores: a lane takes kLane keys (two where
+// several heads' q would else be loaded for one key's worth of work) and its share of their 16-byte
+// columns; q lies in shared memory, column c of a head at c ^ (c / 8 % 8), so that the lanes'
+// columns are in different banks.  The shares are summed by halves that change sides, which leaves
+// each lane one to four of the sums and so the softmax of one or two heads, not of all.  Values:
+// lane l holds the d's of its 16-byte (D = 64: 8-byte) columns; the probabilities and the factors
+// of what is held already come from shared memory, twice each.
 template <int D, int HT> struct F32State {
     using S = Shape<float, D, HT>;
-    static constexpr int KEYS = S::kKeys, kParts = 32 / KEYS, kCols = D / 4, kOwn = D / 32;
-    float m[HT], l[HT], o[HT][kOwn];
+    static constexpr int KEYS = S::kKeys, kLane = HT >= 4 ? 2 : 1, kGroups = KEYS / kLane, kParts = 32 / kGroups;
+    static constexpr int kCols = D / 4, kOwn = D / 32;
+    // A lane's sums after the change of sides: kSums, of kHeads heads and kSums / kHeads keys.  With
+    // one head there is nothing to share out: every part has the sum.
+    static constexpr int kSums = HT == 1 ? 1 : HT * kLane / kParts, kHeads = kSums > kLane ? kSums / kLane : 1;
+    static constexpr int kKeysOwn = kSums / kHeads, kScratch = KEYS * HT + HT;   // float2 of a warp in shared memory
+    static_assert(kSums >= 1 && (HT == 1 || kSums * kParts == HT * kLane), "the sums go round");
+    float m[kHeads], l[kHeads];
+    uint64_t o[HT][kOwn / 2];
 
     __device__ __forceinline__ void start() {
 #pragma unroll
-        for (int h = 0; h < HT; h++) {
+        for (int h = 0; h < kHeads; h++) {
             m[h] = -INFINITY;
             l[h] = 0.f;
-#pragma unroll
-            for (int e = 0; e < kOwn; e++) o[h][e] = 0.f;
         }
+#pragma unroll
+        for (int h = 0; h < HT; h++)
+#pragma unroll
+            for (int e = 0; e < kOwn / 2; e++) o[h][e] = 0ull;
+    }
+    // sum v of a part is of head v / kLane and of the v % kLane-th of its group's keys, v counted
+    // over all parts' sums in order
+    __device__ __forceinline__ static int head(int part, int i) { return HT == 1 ? 0 : (part * kSums + i) / kLane; }
+    __device__ __forceinline__ static int key(int group, int part, int i) {
+        return HT == 1 ? group : group + kGroups * ((part * kSums + i) % kLane);
+    }
+    // over the lanes that hold sums of the same head
+    template <typename F> __device__ __forceinline__ static float over_head(float x, F &&f) {
+#pragma unroll
+        for (int y = kGroups / 2; y >= 1; y >>= 1) x = f(x, __shfl_xor_sync(kFull, x, y));
+        if (HT > 1 && kSums < kLane) x = f(x, __shfl_xor_sync(kFull, x, kGroups));
+        return x;
     }
     // element offset in a row of the lane's own values (kOwn of them: 2, 4 or two times 4)
     __device__ __forceinline__ static int own(int lane, int e) {
         return kOwn == 2 ? 2 * lane + e : 4 * lane + (e & 3) + (e >> 2) * 128;
     }
-    __device__ __forceinline__ void chunk(const uint8_t *stage, const float *sq, float *sp, int left, float scale2,
+    // place of column c of a head in s_q
+    __device__ __forceinline__ static int q_col(int c) { return c ^ ((c >> 3) & 7); }
+    // the i-th column of part p.  Eight lanes read at once: eight groups read one column of rows that
+    // the layout keeps apart, four groups two columns that differ by four.
+    __device__ __forceinline__ static int column(int p, int i) {
+        if (kGroups >= 8) return p + kParts * i;
+        return (i & 3) | ((p & 1) << 2) | (((i >> 2) * (kParts / 2) + (p >> 1)) << 3);
+    }
+    __device__ __forceinline__ void chunk(const uint8_t *stage, const float *sq, float2 *sp, int left, float scale2,
                                           int lane) {
-        const int key = lane % KEYS, part = lane / KEYS;
-        float s[HT];
+        const int group = lane % kGroups, part = lane / kGroups;
+        uint64_t s2[kLane][HT];
 #pragma unroll
-        for (int h = 0; h < HT; h++) s[h] = 0.f;
-#pragma unroll 4
+        for (int k = 0; k < kLane; k++)
+#pragma unroll
+            for (int h = 0; h < HT; h++) s2[k][h] = 0ull;
+#pragma unroll
         for (int i = 0; i < kCols / kParts; i++) {
-            const int c = part + kParts * i;
-            const float4 k = *reinterpret_cast<const float4 *>(stage + key * S::kRowBytes + ((c ^ (key & 7)) << 4));
+            const int c = column(part, i);
+            ulonglong2 x[kLane];
+#pragma unroll
+            for (int k = 0; k < kLane; k++) {
+                const int key = group + kGroups * k;
+                x[k] = *reinterpret_cast<const ulonglong2 *>(stage + key * S::kRowBytes + ((c ^ (key & 7)) << 4));
+            }
 #pragma unroll
             for (int h = 0; h < HT; h++) {
-                const float4 q = *reinterpret_cast<const float4 *>(sq + h * D + 4 * c);
-                s[h] = fmaf(q.x, k.x, s[h]);
-                s[h] = fmaf(q.y, k.y, s[h]);
-                s[h] = fmaf(q.z, k.z, s[h]);
-                s[h] = fmaf(q.w, k.w, s[h]);
+                const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(sq + h * D + 4 * q_col(c));
+#pragma unroll
+                for (int k = 0; k < kLane; k++) {
+                    s2[k][h] = tc::f2_fma(q.x, x[k].x, s2[k][h]);
+                    s2[k][h] = tc::f2_fma(q.y, x[k].y, s2[k][h]);
+                }
             }
         }
+        float v[HT * kLane];
 #pragma unroll
-        for (int h = 0; h < HT; h++) {
+        for (int h = 0; h < HT; h++)
 #pragma unroll
-            for (int x = KEYS; x < 32; x <<= 1) s[h] += __shfl_xor_sync(kFull, s[h], x);
-            s[h] = key < left ? s[h] * scale2 : -INFINITY;
-            float x = s[h];
+            for (int k = 0; k < kLane; k++) {
+                float a, b;
+                tc::f2_unpack(s2[k][h], a, b);
+                v[h * kLane + k] = a + b;
+            }
+        if constexpr (HT == 1) {
 #pragma unroll
-            for (int y = KEYS / 2; y >= 1; y >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, y));
-            const float top = fmaxf(m[h], x), ref = top == -INFINITY ? 0.f : top;
-            const float f = exp2f(m[h] - ref);
-            m[h] = top;
-            s[h] = exp2f(s[h] - ref);
-            l[h] = fmaf(l[h], f, s[h]);
+            for (int y = kGroups; y < 32; y <<= 1) v[0] += __shfl_xor_sync(kFull, v[0], y);
+        } else {
 #pragma unroll
-            for (int e = 0; e < kOwn; e++) o[h][e] *= f;
-            if (part == 0) sp[key * HT + h] = s[h];
+            for (int bit = kParts / 2, half = HT * kLane / 2; bit >= 1; bit >>= 1, half >>= 1) {
+                const bool up = part & bit;
+#pragma unroll
+                for (int j = 0; j < HT * kLane / 2; j++) {
+                    if (j >= half) continue;
+                    const float send = up ? v[j] : v[j + half], keep = up ? v[j + half] : v[j];
+                    v[j] = keep + __shfl_xor_sync(kFull, send, bit * kGroups);
+                }
+            }
         }
+        bool up = false;
+#pragma unroll
+        for (int g = 0; g < kHeads; g++) {
+            float x = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kKeysOwn; k++) {
+                float &s = v[g * kKeysOwn + k];
+                s = key(group, part, g * kKeysOwn + k) < left ? s * scale2 : -INFINITY;
+                x = fmaxf(x, s);
+            }
+            x = over_head(x, [](float a, float b) { return fmaxf(a, b); });
+            const float top = fmaxf(m[g], x), ref = top == -INFINITY ? 0.f : top;
+            const float f = exp2f(m[g] - ref);
+            up |= top != m[g];
+            m[g] = top;
+            l[g] *= f;
+#pragma unroll
+            for (int k = 0; k < kKeysOwn; k++) {
+                const int i = g * kKeysOwn + k;
+                const float p = exp2f(v[i] - ref);
+                l[g] += p;
+                if (HT > 1 || part == 0) sp[key(group, part, i) * HT + head(part, i)] = make_float2(p, p);
+            }
+            if (group == 0) sp[KEYS * HT + head(part, g * kKeysOwn)] = make_float2(f, f);
+        }
+        up = __any_sync(kFull, up);
         __syncwarp();
+        uint64_t w[HT];
+        auto read = [&](const float2 *from) {
+            if constexpr (HT == 1) {
+                w[0] = *reinterpret_cast<const uint64_t *>(from);
+            } else {
+#pragma unroll
+                for (int h = 0; h < HT; h += 2) {
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(from + h);
+                    w[h] = x.x;
+                    w[h + 1] = x.y;
+                }
+            }
+        };
+        if (up) {
+            read(sp + KEYS * HT);
+#pragma unroll
+            for (int h = 0; h < HT; h++)
+#pragma unroll
+                for (int e = 0; e < kOwn / 2; e++) o[h][e] = tc::f2_fma(o[h][e], w[h], 0ull);
+        }
         const uint8_t *v0 = stage + KEYS * S::kRowBytes;
-#pragma unroll 4
+#pragma unroll
         for (int k = 0; k < KEYS; k++) {
-            float v[kOwn];
+            uint64_t x[kOwn / 2];
             if constexpr (kOwn == 2) {
-                const float2 x = *reinterpret_cast<const float2 *>(v0 + k * S::kRowBytes + (((lane >> 1) ^ (k & 7)) << 4) +
-                                                                   (lane & 1) * 8);
-                v[0] = x.x; v[1] = x.y;
+                x[0] = *reinterpret_cast<const uint64_t *>(v0 + k * S::kRowBytes + (((lane >> 1) ^ (k & 7)) << 4) +
+                                                           (lane & 1) * 8);
             } else {
 #pragma unroll
                 for (int g = 0; g < kOwn / 4; g++) {
-                    const float4 x = *reinterpret_cast<const float4 *>(v0 + k * S::kRowBytes +
-                                                                       (((lane + 32 * g) ^ (k & 7)) << 4));
-                    v[4 * g] = x.x; v[4 * g + 1] = x.y; v[4 * g + 2] = x.z; v[4 * g + 3] = x.w;
+                    const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(v0 + k * S::kRowBytes +
+                                                                               (((lane + 32 * g) ^ (k & 7)) << 4));
+                    x[2 * g] = y.x;
+                    x[2 * g + 1] = y.y;
                 }
             }
+            read(sp + k * HT);
 #pragma unroll
-            for (int h = 0; h < HT; h++) {
-                const float p = sp[k * HT + h];
+            for (int h = 0; h < HT; h++)
 #pragma unroll
-                for (int e = 0; e < kOwn; e++) o[h][e] = fmaf(p, v[e], o[h][e]);
-            }
+                for (int e = 0; e < kOwn / 2; e++) o[h][e] = tc::f2_fma(w[h], x[e], o[h][e]);
         }
         __syncwarp();
     }
     __device__ __forceinline__ void finish(float *out, float *sm, float *sl, int lane) {
+        const int group = lane % kGroups, part = lane / kGroups;
 #pragma unroll
-        for (int h = 0; h < HT; h++) {
-            float x = l[h];
-#pragma unroll
-            for (int y = KEYS / 2; y >= 1; y >>= 1) x += __shfl_xor_sync(kFull, x, y);
-            if (lane == 0) {
-                sm[h] = m[h];
-                sl[h] = x;
+        for (int g = 0; g < kHeads; g++) {
+            const float x = over_head(l[g], [](float a, float b) { return a + b; });
+            if (group == 0) {                  // several parts write the same where they share a head
+                sm[head(part, g * kKeysOwn)] = m[g];
+                sl[head(part, g * kKeysOwn)] = x;
             }
-#pragma unroll
-            for (int e = 0; e < kOwn; e++) out[S::out(h, own(lane, e))] = o[h][e];
         }
+#pragma unroll
+        for (int h = 0; h < HT; h++)
+#pragma unroll
+            for (int e = 0; e < kOwn; e += 2) {
+                float a, b;
+                tc::f2_unpack(o[h][e / 2], a, b);
+                out[S::out(h, own(lane, e))] = a;
+                out[S::out(h, own(lane, e + 1))] = b;
+            }
     }
 };
 
@@ -466,8 +590,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
     using S = Shape<T, D, HT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[kWarps][HT], s_l[kWarps][HT], s_fac[HT][33];
-    __shared__ __align__(16) float s_q[S::kTc ? 1 : HT * D];
-    __shared__ float s_p[S::kTc ? 1 : kWarps * S::kKeys * HT];
+    // the row's queries: f32, or a group of 16 heads of 256
+    __shared__ __align__(16) float s_q[!S::kTc ? HT * D : HT * D > 2048 ? HT * D / 2 : 4];
+    __shared__ __align__(16) float2 s_p[S::kTc ? 1 : kWarps * (S::kKeys * HT + HT)];
     __shared__ long long s_sum[kWarps], s_rem;
     __shared__ int s_b, s_last, s_out[kWarps];
     const PagedDev &P = A.P;
@@ -584,16 +709,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
         };
         if constexpr (S::kTc) {
             TcState<T, D, HT> st;
-            st.start(Qr, heads, lane);
-            stream([&](int off, int left) { st.chunk(wst + off, left, A.scale2, lane); });
+            st.start(Qr, heads, reinterpret_cast<uint4 *>(s_q), lane);
+            stream([&](int off, int left) { st.chunk(wst + off, smem_addr(s_q), left, A.scale2, lane); });
             st.finish(reinterpret_cast<float *>(wsm + free * S::kChunkBytes), s_m[warp], s_l[warp], lane);
         } else {
-            for (int x = tid; x < HT * D; x += kThreads) s_q[x] = x / D < heads ? (float)Qr[x] : 0.f;
+            for (int x = tid; x < HT * D; x += kThreads)
+                s_q[x / D * D + 4 * F32State<D, HT>::q_col(x % D / 4) + x % 4] = x / D < heads ? (float)Qr[x] : 0.f;
             __syncthreads();
             F32State<D, HT> st;
             st.start();
             stream([&](int off, int left) {
-                st.chunk(wsm + off, s_q, s_p + warp * S::kKeys * HT, left, A.scale2, lane);
+                st.chunk(wsm + off, s_q, s_p + warp * F32State<D, HT>::kScratch, left, A.scale2, lane);
             });
             st.finish(reinterpret_cast<float *>(wsm + free * S::kChunkBytes), s_m[warp], s_l[warp], lane);
         }

@@ -5,26 +5,30 @@
 // in a stated order, so the result of every call is a function of its inputs: no free list to
 // fall out of step with the tables, no atomics whose order shows.
 //
-// What has to look at all pages (the search for free ones, the packing plan) runs in one CTA of
-// 1024 threads that reads 8192 refs a step, one step ahead, and counts them by a block-wide
-// prefix sum; the search ends with the last page that is wanted.  It is bound by a step's latency
-// (load, two barriers).  What moves data runs on the whole GPU: a warp copies 4 KB at a time, its eight 16-byte
+// What has to look at all pages (the search for free ones, the packing plan) runs in one cluster:
+// a CTA of 512 threads reads 2048 refs a step, one step ahead, and counts them by a block-wide
+// prefix sum; eight such CTAs, where there are more pages than that, exchange their counts
+// through shared memory.  The search ends with the last page that is wanted.  It is bound by a
+// step's latency (load, barriers): the packing plan of 16384 pages takes 7.9 us, in one CTA of 1024 threads 14.4.
+// What moves data runs on the whole GPU: a warp copies 4 KB at a time, its eight 16-byte
 // loads a lane all in flight before the first store; HBM bounds it.
 #include <algorithm>
 
 #include "fs_paged.cuh"
+#include "tc_common.cuh"
 
 namespace fs {
 namespace {
 
 constexpr int kMaxPages = 2000000;             // kPlanThreads times as many fit an int
-constexpr int kPlanThreads = 1024, kPerThread = 8, kPlanStep = kPlanThreads * kPerThread;
+constexpr int kPlanThreads = 512, kPerThread = 4, kPlanStep = kPlanThreads * kPerThread;
+constexpr int kFreeThreads = 1024;
 constexpr int kCopyThreads = 256, kCopyAhead = 8, kSlab = 32 * kCopyAhead;     // vectors a warp copies at once
 
 // ---- lists in the workspace's area, in ints
 enum : int { kOk = 0, kMoves = 1, kLive = 2, kHead = 16 };
 
-// Inclusive sum over the block of 1024 threads; `total` receives the sum.  s: 33 shared ints.
+// Inclusive sum over the block of kPlanThreads; `total` receives the sum.  s: 32 shared ints.
 __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -37,7 +41,7 @@ __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
     if (lane == 31) s[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int w = s[lane];
+        int w = lane < kPlanThreads / 32 ? s[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(kFull, w, o);
@@ -49,6 +53,40 @@ __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
     total = s[31];
     return x + (warp ? s[warp - 1] : 0);
 }
+
+// The CTAs of the cluster exchange a number: the sum of those before this one, and of all.
+// Called by every thread of every CTA, `v` the same in a CTA.  slot: shared ints, two by turns.
+struct Cluster {
+    int rank, size, turn;
+    __device__ __forceinline__ Cluster() : turn(0) {
+        asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+        asm("mov.u32 %0, %cluster_nctarank;" : "=r"(size));
+    }
+    __device__ __forceinline__ void exchange(int v, int *slot, int &before, int &all) {
+        before = 0;
+        all = v;
+        if (size == 1) {
+            __syncthreads();
+            return;
+        }
+        int *mine = slot + turn;
+        turn ^= 1;                             // a slow reader of this one is past it when it comes round again
+        if (threadIdx.x == 0) *mine = v;
+        tc::cluster_sync();
+        all = 0;
+        for (int r = 0; r < size; r++) {
+            int x;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(tc::cluster_map(tc::smem_u32(mine), r)) : "memory");
+            if (r < rank) before += x;
+            all += x;
+        }
+    }
+    // also keeps a CTA's shared memory until all have read it
+    __device__ __forceinline__ void sync() const {
+        if (size == 1) __syncthreads();
+        else tc::cluster_sync();
+    }
+};
 
 // refs of the pages first .. first + 7; pages past the last read as in use
 __device__ __forceinline__ void load_refs(const int32_t *refs, int first, int n, int (&r)[kPerThread]) {
@@ -65,26 +103,29 @@ __device__ __forceinline__ void load_refs(const int32_t *refs, int first, int n,
 }
 
 // The `want` lowest free pages, ascending, to list; returns how many there are (at most want).
-__device__ int find_free(const int32_t *refs, int n, int want, int *list, int *s) {
+// The list is complete for every CTA.
+__device__ int find_free(const int32_t *refs, int n, int want, int *list, int *s, int *slot, Cluster &cl) {
     int found = 0;
     int next[kPerThread];
-    const int mine = (int)threadIdx.x * kPerThread;
-    load_refs(refs, mine, n, next);
-    for (int base = 0; base < n && found < want; base += kPlanStep) {
-        int r[kPerThread], k = 0, total;
+    const int mine = (cl.rank * kPlanThreads + (int)threadIdx.x) * kPerThread, step = cl.size * kPlanStep;
+    load_refs(refs, min(mine, n), n, next);
+    for (int base = 0; base < n && found < want; base += step) {
+        int r[kPerThread], k = 0, total, before, all;
 #pragma unroll
         for (int i = 0; i < kPerThread; i++) {
             r[i] = next[i];
             k += r[i] == 0;
         }
-        if (base + kPlanStep < n) load_refs(refs, min(base + kPlanStep + mine, n), n, next);
-        int at = found + block_scan(k, s, total) - k;
+        if (base + step < n) load_refs(refs, min(base + step + mine, n), n, next);
+        const int incl = block_scan(k, s, total);
+        cl.exchange(total, slot, before, all);
+        int at = found + before + incl - k;
 #pragma unroll
         for (int i = 0; i < kPerThread; i++)
             if (r[i] == 0 && at < want) list[at++] = base + mine + i;
-        found += total;
+        found += all;
     }
-    __syncthreads();                           // the list is complete
+    cl.sync();
     return min(found, want);
 }
 
@@ -92,50 +133,52 @@ __device__ int find_free(const int32_t *refs, int n, int want, int *list, int *s
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_constant__ PagedDev P,
                                                                const int32_t *n_new, int32_t *refs, int32_t *table,
                                                                int32_t *lens, int *area, int *flag) {
-    __shared__ int s[33];
+    __shared__ int s[32], slot[2];
+    Cluster cl;
     griddep_wait();
     int *offs = area + kHead, *list = offs + P.B + 1;
     const int tid = threadIdx.x;
-    // pages that each sequence needs, summed before it
+    // the first CTA sums the pages that the sequences before each one need
     bool bad = false;
-    long long want = 0;
-    for (int base = 0; base < P.B; base += kPlanThreads) {
-        const int b = base + tid;
-        int need = 0, total;
-        if (b < P.B) {
-            const int n = n_new[b], len = lens[b];
-            if (n < 0 || len < 0 || (long long)len + n > P.cap) bad = true;
-            else need = P.pages_of(len + n) - P.pages_of(len);
+    long long sum = 0;
+    if (cl.rank == 0) {
+        for (int base = 0; base < P.B; base += kPlanThreads) {
+            const int b = base + tid;
+            int need = 0, total;
+            if (b < P.B) {
+                const int n = n_new[b], len = lens[b];
+                if (n < 0 || len < 0 || (long long)len + n > P.cap) bad = true;
+                else need = P.pages_of(len + n) - P.pages_of(len);
+            }
+            need = min(need, P.num_pages + 1); // more than there are; a block's sum fits an int
+            const int before = block_scan(need, s, total) - need;
+            if (b < P.B) offs[b] = (int)min(sum + before, 0x7fffffffll);
+            sum += total;
         }
-        need = min(need, P.num_pages + 1);     // more than there are; 1024 of them fit an int
-        const int before = block_scan(need, s, total) - need;
-        if (b < P.B) offs[b] = (int)min(want + before, 0x7fffffffll);
-        want += total;
+        bad |= sum > P.num_pages;
+        bad = __syncthreads_or(bad);
     }
-    if (tid == 0) offs[P.B] = (int)min(want, 0x7fffffffll);
-    bad |= want > P.num_pages;
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) raise_check(flag);
-        return;
-    }
-    const int w = (int)want;
-    if (find_free(refs, P.num_pages, w, list, s) < w) {
-        if (tid == 0) raise_check(flag);
-        return;
-    }
-    for (int i = tid; i < w; i += kPlanThreads) {
-        int lo = 0, hi = P.B;                  // the last b with offs[b] <= i
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (offs[mid] <= i) lo = mid;
-            else hi = mid;
+    int before, want;
+    cl.exchange(bad ? -1 : (int)sum, slot, before, want);      // the others add 0
+    if (want > 0 && find_free(refs, P.num_pages, want, list, s, slot, cl) < want) want = -1;
+    if (want < 0) {
+        if (cl.rank == 0 && tid == 0) raise_check(flag);
+    } else {
+        for (int i = cl.rank * kPlanThreads + tid; i < want; i += cl.size * kPlanThreads) {
+            int lo = 0, hi = P.B;              // the last b with offs[b] <= i
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (__ldcg(offs + mid) <= i) lo = mid;
+                else hi = mid;
+            }
+            const int page = __ldcg(list + i);
+            table[(long long)lo * P.max_pages + P.pages_of(lens[lo]) + (i - __ldcg(offs + lo))] = page;
+            refs[page] = 1;
         }
-        const int page = list[i];
-        table[(long long)lo * P.max_pages + P.pages_of(lens[lo]) + (i - offs[lo])] = page;
-        refs[page] = 1;
     }
-    __syncthreads();                           // lens has been read
-    for (int b = tid; b < P.B; b += kPlanThreads) lens[b] += n_new[b];
+    cl.sync();                                 // lens has been read
+    if (want >= 0 && cl.rank == 0)
+        for (int b = tid; b < P.B; b += kPlanThreads) lens[b] += n_new[b];
 }
 
 // A page's elements in 16-byte vectors: `outer` x `inner` runs of `run` vectors.
@@ -195,69 +238,80 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const __grid_constant__ PagedDev P, int32_t *refs,
                                                                  int32_t *lens, const int32_t *src, const int32_t *dst,
                                                                  int n, int *area, int *flag) {
-    __shared__ int s[33];
+    __shared__ int s[32], slot[2];
+    Cluster cl;
     griddep_wait();
     int *tail = area + kHead, *list = tail + n, *held = list + P.num_pages;
     const int tid = threadIdx.x;
-    // each dst is claimed by its lens, which has to be 0: neither in use nor listed twice
     bool bad = false;
-    for (int i = tid; i < n; i += kPlanThreads) {
-        const int d = dst[i];
-        held[i] = 0;
-        if ((unsigned)src[i] >= (unsigned)P.B || (unsigned)d >= (unsigned)P.B) bad = true;
-        else if (atomicCAS(lens + d, 0, -1) != 0) bad = true;
-        else held[i] = 1;
-    }
-    bad = __syncthreads_or(bad);
-    // a src that is a dst too has the length -1 now
-    int want = 0;
-    for (int base = 0; base < n && !bad; base += kPlanThreads) {
-        const int i = base + tid;
-        int part = 0, total;
-        bool wrong = false;
-        if (i < n) {
-            const int len = __ldcg(lens + src[i]);
-            int q, r = 0;
-            wrong = len < 0 || len > P.cap;
-            if (!wrong) P.locate(len, q, r);
-            part = r > 0;
+    int sum = 0;
+    if (cl.rank == 0) {                        // the pairs are the first CTA's
+        // each dst is claimed by its lens, which has to be 0: neither in use nor listed twice
+        for (int i = tid; i < n; i += kPlanThreads) {
+            const int a = src[i], d = dst[i];
+            held[i] = 0;
+            if ((unsigned)a >= (unsigned)P.B || (unsigned)d >= (unsigned)P.B) bad = true;
+            else if (atomicCAS(lens + d, 0, -1) != 0) bad = true;
+            else held[i] = 1;
         }
-        bad = __syncthreads_or(wrong);
-        const int at = want + block_scan(part, s, total) - part;
-        if (i < n) tail[i] = part ? at : -1;
-        want += total;
+        bad = __syncthreads_or(bad);
+        // a src that is a dst too has the length -1 now
+        for (int base = 0; base < n && !bad; base += kPlanThreads) {
+            const int i = base + tid;
+            int part = 0, total;
+            bool wrong = false;
+            if (i < n) {
+                const int len = __ldcg(lens + src[i]);
+                int q, r = 0;
+                wrong = len < 0 || len > P.cap;
+                if (!wrong) P.locate(len, q, r);
+                part = r > 0;
+            }
+            bad = __syncthreads_or(wrong);
+            const int at = sum + block_scan(part, s, total) - part;
+            if (i < n) tail[i] = part ? at : -1;
+            sum += total;
+        }
     }
-    if (!bad) bad = find_free(refs, P.num_pages, want, list, s) < want;
-    __syncthreads();
-    for (int i = tid; i < n; i += kPlanThreads) {
-        if (bad) {
-            if (held[i]) lens[dst[i]] = 0;
-        } else {
-            lens[dst[i]] = __ldcg(lens + src[i]);
-            if (tail[i] >= 0) {
-                tail[i] = list[tail[i]];
-                refs[tail[i]] = 1;
+    int before, want;
+    cl.exchange(bad ? -1 : sum, slot, before, want);           // the others add 0
+    if (want > 0 && find_free(refs, P.num_pages, want, list, s, slot, cl) < want) want = -1;
+    if (cl.rank == 0) {
+        __syncthreads();
+        for (int i = tid; i < n; i += kPlanThreads) {
+            if (want < 0) {
+                if (held[i]) lens[dst[i]] = 0;
+            } else {
+                lens[dst[i]] = __ldcg(lens + src[i]);
+                if (tail[i] >= 0) {
+                    const int page = __ldcg(list + tail[i]);
+                    tail[i] = page;
+                    refs[page] = 1;
+                }
             }
         }
+        if (tid == 0) {
+            area[kOk] = want >= 0;
+            if (want < 0) raise_check(flag);
+        }
     }
-    if (tid == 0) {
-        area[kOk] = !bad;
-        if (bad) raise_check(flag);
-    }
+    cl.sync();
 }
 
 // Fork, second part: rows, references and the tails' tokens.
-__global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constant__ PagedDev P, int vec, uint4 *Kp,
+__global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constant__ PagedDev P, int shift, uint4 *Kp,
                                                             uint4 *Vp, int32_t *refs, int32_t *table,
                                                             const int32_t *lens, const int32_t *src, const int32_t *dst,
                                                             const int *area, int *flag) {
     griddep_wait();
-    if (!area[kOk]) return;
-    const int i = blockIdx.x, len = lens[src[i]];
-    const int32_t *from = table + (long long)src[i] * P.max_pages;
-    int32_t *to = table + (long long)dst[i] * P.max_pages;
+    const int i = blockIdx.x, ok = area[kOk], a_row = src[i], b_row = dst[i], b = (area + kHead)[i];
+    if (!ok) return;
+    const int len = lens[a_row];
+    const int32_t *from = table + (long long)a_row * P.max_pages;
+    int32_t *to = table + (long long)b_row * P.max_pages;
     int whole, part;
     P.locate(len, whole, part);
+    const int a = part ? from[whole] : 0;
     const int t0 = blockIdx.y * kCopyThreads + threadIdx.x, step = gridDim.y * kCopyThreads;
     for (int k = t0; k < whole; k += step) {
         const int page = from[k];
@@ -266,17 +320,17 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constan
         else raise_check(flag);
     }
     if (part == 0) return;
-    const int a = from[whole], b = (area + kHead)[i];
     if (t0 == 0) to[whole] = b;
     if (!P.page_ok(a)) {
         raise_check(flag);
         return;
     }
     // the tokens that the page holds: (head, slot, vector), both pools
-    const int cols = P.d / vec, n = P.Hkv * part * cols;
+    const int cols = P.d >> shift, n = P.Hkv * part * cols;
+    const long long sp = P.sp >> shift, sh = P.sh >> shift, st = P.st >> shift;
     for (int x = t0; x < n; x += step) {
         const int row = x / cols, h = row / part;
-        const long long at = (h * P.sh + (row - h * part) * P.st) / vec + (x - row * cols), sp = P.sp / vec;
+        const long long at = h * sh + (row - h * part) * st + (x - row * cols);
         const uint4 k = Kp[a * sp + at], v = Vp[a * sp + at];
         Kp[b * sp + at] = k;
         Vp[b * sp + at] = v;
@@ -284,7 +338,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constan
 }
 
 // One CTA per listed sequence; the first to take its length frees it.
-__global__ void __launch_bounds__(kPlanThreads) free_kernel(const __grid_constant__ PagedDev P, int32_t *refs,
+__global__ void __launch_bounds__(kFreeThreads) free_kernel(const __grid_constant__ PagedDev P, int32_t *refs,
                                                             int32_t *table, int32_t *lens, const int32_t *rows,
                                                             int *flag) {
     __shared__ int s_len;
@@ -305,7 +359,7 @@ __global__ void __launch_bounds__(kPlanThreads) free_kernel(const __grid_constan
     __syncthreads();
     const int n = P.pages_of(s_len);
     int32_t *row = table + (long long)b * P.max_pages;
-    for (int k = threadIdx.x; k < n; k += kPlanThreads) {
+    for (int k = threadIdx.x; k < n; k += kFreeThreads) {
         const int page = row[k];
         row[k] = -1;
         if (!P.page_ok(page)) {
@@ -321,33 +375,41 @@ __global__ void __launch_bounds__(kPlanThreads) free_kernel(const __grid_constan
 // rank[page] of the latter (-1: a free page there) and their refs.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ PagedDev P,
                                                                     const int32_t *refs, int32_t *live_out, int *area) {
-    __shared__ int s[33];
+    __shared__ int s[32], slot[2];
+    Cluster cl;
     griddep_wait();
-    const int n = P.num_pages, tid = threadIdx.x, mine = tid * kPerThread;
+    const int n = P.num_pages, mine = (cl.rank * kPlanThreads + (int)threadIdx.x) * kPerThread;
+    const int step = cl.size * kPlanStep;
     int *hole = area + kHead, *mover = hole + n, *count = mover + n, *rank = count + n;
-    int used = 0, live;
-    for (int base = 0; base < n; base += kPlanStep) {
+    int used = 0, total, before, live;
+    int next[kPerThread];
+    for (int base = 0; base < n; base += step) {
         int r[kPerThread];
         load_refs(refs, min(base + mine, n), n, r);
 #pragma unroll
-        for (int i = 0; i < kPerThread; i++) used += base + mine + i < n && r[i] > 0;
+        for (int i = 0; i < kPerThread; i++) {
+            used += base + mine + i < n && r[i] > 0;
+            if (base == 0) next[i] = r[i];     // the first step's are the next loop's first
+        }
     }
-    block_scan(used, s, live);
+    block_scan(used, s, total);
+    cl.exchange(total, slot, before, live);
     int holes = 0, movers = 0;
-    int next[kPerThread];
-    load_refs(refs, min(mine, n), n, next);
-    for (int base = 0; base < n; base += kPlanStep) {
-        int r[kPerThread], k = 0, total;
+    for (int base = 0; base < n; base += step) {
+        int r[kPerThread], k = 0;
 #pragma unroll
         for (int i = 0; i < kPerThread; i++) {
             const int page = base + mine + i;
             r[i] = next[i];
             if (page < live) k += r[i] <= 0 ? 1 : 0;
-            else if (page < n) k += r[i] > 0 ? 1 << 16 : 0;        // both counts of a step fit 16 bits
+            else if (page < n) k += r[i] > 0 ? 1 << 16 : 0;        // both counts of a CTA's step fit 16 bits
         }
-        if (base + kPlanStep < n) load_refs(refs, min(base + kPlanStep + mine, n), n, next);
-        const int before = block_scan(k, s, total) - k;
-        int ah = holes + (before & 0xffff), am = movers + (before >> 16);
+        if (base + step < n) load_refs(refs, min(base + step + mine, n), n, next);
+        const int here = block_scan(k, s, total) - k;
+        int hb, ha, mb, ma;
+        cl.exchange(total & 0xffff, slot, hb, ha);
+        cl.exchange(total >> 16, slot, mb, ma);
+        int ah = holes + hb + (here & 0xffff), am = movers + mb + (here >> 16);
 #pragma unroll
         for (int i = 0; i < kPerThread; i++) {
             const int page = base + mine + i;
@@ -361,14 +423,15 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
                 }
             }
         }
-        holes += total & 0xffff;
-        movers += total >> 16;
+        holes += ha;
+        movers += ma;
     }
-    if (tid == 0) {
+    if (cl.rank == 0 && threadIdx.x == 0) {
         area[kMoves] = movers;                 // as many as there are holes
         area[kLive] = live;
         if (live_out) *live_out = live;
     }
+    cl.sync();
 }
 
 // Packing, second part: the pages, the refs, the table.
@@ -435,6 +498,25 @@ PageShape page_shape(const PagedDev &P, fs_dtype dt) {
 unsigned copy_grid(const PageShape &G, long long pages) {
     const long long tasks = 2 * pages * ((G.vecs + kSlab - 1) / kSlab), warps = kCopyThreads / 32;
     return (unsigned)std::max(1ll, std::min((tasks + warps - 1) / warps, 148ll * 8));
+}
+
+// One cluster: a CTA where it reads all refs in one step, else eight.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_plan(void (*kern)(KArgs...), int num_pages, cudaStream_t st, Args &&...args) {
+    const unsigned n = num_pages <= kPlanStep ? 1 : 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = n;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 int *area_of(void *ws) { return reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + kPagedArea); }
@@ -508,7 +590,7 @@ extern "C" fs_status fs_pages_reserve(const fs_paged_params *p, const int32_t *n
     if (!n_new || !refs || !table || !lens || !aligned16(refs)) return FS_ERR_INVALID_ARG;
     const cudaStream_t st = (cudaStream_t)stream;
     LaunchScope scope(kPagesReserve, st);
-    return done(launch_pdl(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, st, P, n_new, refs, table, lens, area_of(ws),
+    return done(launch_plan(reserve_kernel, P.num_pages, st, P, n_new, refs, table, lens, area_of(ws),
                            static_cast<int *>(ws)));
 }
 
@@ -541,7 +623,7 @@ extern "C" fs_status fs_pages_fork(const fs_paged_params *p, void *Kp, void *Vp,
     int *flag = static_cast<int *>(ws);
     {
         LaunchScope scope(kPagesForkPlan, st);
-        const cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, P, refs, lens, src, dst, n,
+        const cudaError_t e = launch_plan(fork_plan_kernel, P.num_pages, st, P, refs, lens, src, dst, n,
                                          area_of(ws), flag);
         if (e != cudaSuccess) return FS_ERR_CUDA;
     }
@@ -550,7 +632,7 @@ extern "C" fs_status fs_pages_fork(const fs_paged_params *p, void *Kp, void *Vp,
     const long long work = std::max<long long>((long long)p->Hkv * p->page_size * (p->d / vec), p->max_pages);
     const unsigned gy = (unsigned)std::max(1ll, std::min(std::min(work / (4 * kCopyThreads), 148ll * 8 / n + 1), 64ll));
     LaunchScope scope(kPagesFork, st);
-    return done(launch_pdl(fork_kernel, dim3(n, gy), dim3(kCopyThreads), 0, st, P, vec, (uint4 *)Kp, (uint4 *)Vp, refs,
+    return done(launch_pdl(fork_kernel, dim3(n, gy), dim3(kCopyThreads), 0, st, P, p->dtype == FS_F32 ? 2 : 3, (uint4 *)Kp, (uint4 *)Vp, refs,
                            table, (const int32_t *)lens, src, dst, (const int *)area_of(ws), flag));
 }
 
@@ -564,7 +646,7 @@ extern "C" fs_status fs_pages_free(const fs_paged_params *p, int32_t *refs, int3
     if (!refs || !table || !lens || !rows) return FS_ERR_INVALID_ARG;
     const cudaStream_t st = (cudaStream_t)stream;
     LaunchScope scope(kPagesFree, st);
-    return done(launch_pdl(free_kernel, dim3(n), dim3(kPlanThreads), 0, st, P, refs, table, lens, rows,
+    return done(launch_pdl(free_kernel, dim3(n), dim3(kFreeThreads), 0, st, P, refs, table, lens, rows,
                            static_cast<int *>(ws)));
 }
 
@@ -580,7 +662,7 @@ extern "C" fs_status fs_pages_compact(const fs_paged_params *p, void *Kp, void *
     const cudaStream_t st = (cudaStream_t)stream;
     {
         LaunchScope scope(kPagesCompactPlan, st);
-        const cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, P, refs, live, area_of(ws));
+        const cudaError_t e = launch_plan(compact_plan_kernel, P.num_pages, st, P, refs, live, area_of(ws));
         if (e != cudaSuccess) return FS_ERR_CUDA;
     }
     const long long rows = std::max<long long>(P.num_pages, (long long)P.B * P.max_pages);
