@@ -377,15 +377,17 @@ fs_status fs_rope_backward(const fs_rope_params *p, const fs_rotary *rot, const 
  * that the caller owns; a new cache has table = -1, lens = 0, refs = 0.
  *
  * Supported: d = 64, 128 or 256; H a multiple of Hkv; any page_size >= 1 with
- * max_pages page_size < 2^30; num_pages <= 2,000,000; strides that are multiples of 16 bytes and keep the elements of a
- * pool apart (pools of any size: offsets are 64-bit); dtype bf16, f16 or f32.
+ * max_pages page_size < 2^30; num_pages <= 2,000,000; strides that are multiples of 16 bytes and
+ * keep the elements of a pool apart (pools of any size: offsets are 64-bit); dtype bf16, f16 or
+ * f32.
  *
  * ws: fs_paged_workspace_size bytes of device workspace, zero-filled once; its first bytes hold
  * the device error flag read by fs_sync_status.  Calls that share a workspace must be ordered
- * (one stream, or graphs that do not overlap); between calls it carries nothing but the flag.
- * A table entry outside [0, num_pages) that a call needs, a length outside
- * [0, max_pages page_size] and the like set the flag (FS_ERR_KERNEL_CHECK); no call reads or
- * writes outside the pools for them. */
+ * (one stream, or graphs that do not overlap); between calls it carries nothing but the flag,
+ * and one made for the largest B, num_pages and d serves smaller ones.  Every call can be
+ * captured into a graph: lens, table and the lists are read when it runs.  A table entry outside
+ * [0, num_pages) that a call needs, a length outside [0, max_pages page_size] and the like set
+ * the flag (FS_ERR_KERNEL_CHECK); no call reads or writes outside the pools for them. */
 typedef struct {
     int B;                    /* sequences: rows of table and lens */
     int H, Hkv, d;            /* query heads, key-value heads, head dim */
@@ -414,11 +416,15 @@ fs_status fs_paged_append(const fs_paged_params *p, const fs_rotary *rot, int T,
  * sees the keys j in [max(0, lens[b] - 1 - window), lens[b] - 1] (window < 0: all),
  *     O[b,h] = sum_j softmax_j(scale q.k_j) v_j  with the keys of head h / (H / Hkv),
  *     lse[b,h] = log sum_j exp(scale q.k_j)   (float32, NULL: not wanted).
- * Q, O: [B, H, d], rows b q_stride / o_stride elements apart, heads d apart.  With keys written
- * rotated and window = w this is o^sr of eq. (3).  lens[b] = 0: O = 0 and lse = -inf.
- * bf16, f16: products on the tensor cores, fp32 softmax and sums, the probabilities rounded to
- * the type for the product with V; f32: fp32 throughout.  What pages hold behind the last token
- * is never used, NaN included. */
+ * Q, O: [B, H, d], rows b q_stride / o_stride elements apart (on 16-byte boundaries), heads d
+ * apart; O and lse overlap no input.  0 < scale <= 1e30.  B H (span / 64 + 1) < 2^36, span the
+ * most tokens that a sequence can see.  With keys written rotated and window = w this is o^sr of
+ * eq. (3).  lens[b] = 0: O = 0 and lse = -inf.  A sequence with a bad entry or length (flagged)
+ * has undefined outputs.
+ * bf16, f16: products on the tensor cores, fp32 softmax and sums, the probabilities in two parts
+ * of the type for the product with V (2^-16 of them is lost); f32: fp32 throughout.  What pages
+ * hold behind the last token is never used, NaN included; an infinite value of V that is seen
+ * makes its outputs infinite or NaN. */
 fs_status fs_paged_attend(const fs_paged_params *p, const void *Q, long long q_stride, const void *Kp, const void *Vp,
                           const int32_t *table, const int32_t *lens, int window, float scale, void *O,
                           long long o_stride, float *lse, void *ws, size_t ws_bytes, void *stream);
@@ -432,7 +438,7 @@ fs_status fs_pages_reserve(const fs_paged_params *p, const int32_t *n_new, int32
                            int32_t *lens, void *ws, size_t ws_bytes, void *stream);
 
 /* Page dst[i] becomes a copy of page src[i] in both pools, i < n (device int32).  The dst pages
- * are distinct and none of them is a src. */
+ * are distinct and none of them is a src (not checked: such a page's bytes are undefined). */
 fs_status fs_pages_copy(const fs_paged_params *p, void *Kp, void *Vp, const int32_t *src, const int32_t *dst, int n,
                         void *ws, size_t ws_bytes, void *stream);
 

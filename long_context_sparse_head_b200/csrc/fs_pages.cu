@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
         load_refs(refs, min(base + mine, n), n, r);
 #pragma unroll
         for (int i = 0; i < kPerThread; i++) {
-            used += base + mine + i < n && r[i] > 0;
+            used += base + mine + i < n && r[i] != 0;
             if (base == 0) next[i] = r[i];     // the first step's are the next loop's first
         }
     }
@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
         for (int i = 0; i < kPerThread; i++) {
             const int page = base + mine + i;
             r[i] = next[i];
-            if (page < live) k += r[i] <= 0 ? 1 : 0;
-            else if (page < n) k += r[i] > 0 ? 1 << 16 : 0;        // both counts of a CTA's step fit 16 bits
+            if (page < live) k += r[i] == 0 ? 1 : 0;
+            else if (page < n) k += r[i] != 0 ? 1 << 16 : 0;        // both counts of a CTA's step fit 16 bits
         }
         if (base + step < n) load_refs(refs, min(base + step + mine, n), n, next);
         const int here = block_scan(k, s, total) - k;
@@ -414,10 +414,10 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
         for (int i = 0; i < kPerThread; i++) {
             const int page = base + mine + i;
             if (page < live) {
-                if (r[i] <= 0) hole[ah++] = page;
+                if (r[i] == 0) hole[ah++] = page;
             } else if (page < n) {
-                rank[page] = r[i] > 0 ? am : -1;
-                if (r[i] > 0) {
+                rank[page] = r[i] != 0 ? am : -1;
+                if (r[i] != 0) {
                     mover[am] = page;
                     count[am++] = r[i];
                 }
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const __grid_cons
         for (long long x = t0; x < n; x += step) {
             const int r = refs[x];
             if (x >= live) refs_out[x] = 0;
-            else if (r > 0) refs_out[x] = r;
+            else if (r != 0) refs_out[x] = r;
         }
     for (long long x = t0; x < moves; x += step) {
         refs_out[hole[x]] = count[x];

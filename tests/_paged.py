@@ -57,7 +57,8 @@ def attend(q, k, v, scale):
 def attend_bounds(q, k, o, lse, absv, scale, dtype):
     """Bounds on o and lse.  A score is a sum of d products kept in fp32 (an ulp of the running sum
     at each step: d 2^-23 sum|q k|), and its exponent is rounded at 2^-23 of its size; a
-    probability is rounded to the type (half a step); sums over n tokens lose at most an ulp each."""
+    probability goes into the product in two parts of the type (half a step of half a step, under
+    2^-16); sums over n tokens lose at most an ulp each."""
     n, d = k.shape
     if n == 0:
         return np.zeros_like(o), np.zeros_like(lse)
@@ -65,9 +66,9 @@ def attend_bounds(q, k, o, lse, absv, scale, dtype):
     score = size * (d + 4) * 2.0 ** -23 + 2.0 ** -20
     sums = n * 2.0 ** -23
     half = HALF_STEP[dtype]
-    rel = 2 * score + sums + (0.0 if dtype == "f32" else half)
+    rel = 2 * score + sums + (0.0 if dtype == "f32" else 2.0 ** -16)
     tiny = 2.0 ** -25 if dtype == "f16" else 0.0
-    # fp16 probabilities below 2^-14 are held in steps of 2^-24 of the largest: half a step on each
+    # the second part of an fp16 probability is held in steps of 2^-24: half a step on each
     if dtype == "f16":
         rel = rel + n * 2.0 ** -25
     return absv * rel[:, None] + np.abs(o) * half + tiny, score + sums + np.abs(lse) * 2.0 ** -22

@@ -59,6 +59,10 @@ def test_attend_refused(kw, code):
     assert attend(paged(), **kw) == code
 
 
+def test_attend_of_too_much_refused():
+    assert attend(paged(B=1 << 20, max_pages=1 << 25)) == 2
+
+
 def append(p, **kw):
     a = dict(rot=None, T=2, Q=None, qs=0, Qo=None, qos=0, k=PTR, ks=128, v=PTR, vs=128, cu=None, K=PTR, V=PTR, table=PTR,
              lens=PTR, ws=PTR, n=1 << 30)
