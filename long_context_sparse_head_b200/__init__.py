@@ -385,23 +385,22 @@ def _refuse(where, what):
     raise FsError(1, "%s: %s" % (where, what))
 
 
-_torch = _raw_stream = None
+_torch = _raw_stream = _raw_device = None
+_DTYPES = {}
 
 
 def _types():
     """torch, once it is imported, and the element types of the serving calls."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _raw_device
     if _torch is None:
         import torch
-        # the current stream's handle; the public call makes an object for it, 1.2 us
+        # handles of the current stream and device (the public call makes a stream object, 1.2 us)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        _torch = torch
+        _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _DTYPES.update({torch.bfloat16: FS_BF16, torch.float32: FS_F32, torch.float16: FS_F16})
+        _torch = torch
     return _torch
-
-
-_DTYPES = {}
 
 
 def _dtype(t, where):
@@ -415,18 +414,19 @@ def _dtype(t, where):
 
 def _run(fn, where, stream, tensors, *args):
     """fn(*args, stream) with the tensors' device current; on that device's current stream unless given."""
-    torch = _torch or _types()
     dev = tensors[0].get_device()
     if dev < 0:
         _refuse(where, "tensors are on a CUDA device")
     for t in tensors:
         if t.get_device() != dev:
             _refuse(where, "all tensors are on one device")
+    if _torch is None:
+        _types()
     stream = _raw_stream(dev) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev:
+    if _raw_device() == dev:
         code = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with _torch.cuda.device(dev):
             code = fn(*args, stream)
     if code:
         raise FsError(code, where)
@@ -515,6 +515,9 @@ class PagedParams:
         self.scale = d ** -0.5 if d > 0 else 0.0
         self.stride4, self.table_shape, self.table_stride = self.strides + (1,), (B, max_pages), (max_pages, 1)
         self.code = {"bf16": FS_BF16, "f32": FS_F32, "f16": FS_F16}[dtype]
+        torch = _types()
+        self.dt = {"bf16": torch.bfloat16, "f32": torch.float32, "f16": torch.float16}[dtype]
+        self.int32, self.row_shape, self.lens_shape = torch.int32, (B, H, d), (B,)
         self.c = FsPagedParams(B, H, Hkv, d, page_size, num_pages, max_pages, *self.strides, self.code)
         paged_workspace_size(self)             # refuses what is not supported
 
@@ -537,22 +540,22 @@ def alloc_paged_workspace(params, device="cuda"):
 def alloc_pages(params, device="cuda"):
     """An empty cache: pools Kp, Vp (contents undefined), refs, table and lens."""
     import torch
-    dt = {"bf16": torch.bfloat16, "f32": torch.float32, "f16": torch.float16}[params.dtype]
     size = sum((n - 1) * s for n, s in zip(params.shape, params.strides)) + params.d
-    Kp, Vp = (torch.empty(size, dtype=dt, device=device).as_strided(params.shape, params.strides + (1,))
+    Kp, Vp = (torch.empty(size, dtype=params.dt, device=device).as_strided(params.shape, params.strides + (1,))
               for _ in range(2))
     refs = torch.zeros(params.num_pages, dtype=torch.int32, device=device)
     table = torch.full((params.B, params.max_pages), -1, dtype=torch.int32, device=device)
     return Kp, Vp, refs, table, torch.zeros(params.B, dtype=torch.int32, device=device)
 
 
-def _pools(p, where, *pools):
-    for t in pools:
-        if t.shape != p.shape or _dtype(t, where) != p.code:
-            _refuse(where, "pools have the shape and type of the parameters")
-        st = t.stride()
-        if st != p.stride4 and (st[3] != 1 or any(n > 1 and a != b for n, a, b in zip(p.shape, st, p.strides))):
-            _refuse(where, "pools have the strides of the parameters")
+def _pools(p, where, Kp, Vp):
+    if not Kp.shape == Vp.shape == p.shape or Kp.dtype is not p.dt or Vp.dtype is not p.dt:
+        _refuse(where, "pools have the shape and type of the parameters")
+    if not Kp.stride() == Vp.stride() == p.stride4:
+        for t in (Kp, Vp):                     # the stride of a dimension of one says nothing
+            st = t.stride()
+            if st[3] != 1 or any(n > 1 and a != b for n, a, b in zip(p.shape, st, p.strides)):
+                _refuse(where, "pools have the strides of the parameters")
 
 
 def _ints(where, n, *tensors):
@@ -562,16 +565,18 @@ def _ints(where, n, *tensors):
             _refuse(where, "a list is contiguous int32 of the length that goes with the others")
 
 
-def _table(p, where, t):
-    if t.dtype is not (_torch or _types()).int32 or t.shape != p.table_shape or not (
-            t.stride() == p.table_stride or t.is_contiguous()):
+def _table(p, where, table, lens=None):
+    if table.dtype is not p.int32 or table.shape != p.table_shape or not (
+            table.stride() == p.table_stride or table.is_contiguous()):
         _refuse(where, "table is contiguous int32 [B, max_pages]")
+    if lens is not None and (lens.dtype is not p.int32 or lens.shape != p.lens_shape or not lens.is_contiguous()):
+        _refuse(where, "lens is contiguous int32 [B]")
 
 
-def _rows(p, where, t, heads, rows):
+def _rows(p, where, t, shape):
     """A [rows, heads, d] tensor with heads d apart: its row stride."""
     st = t.stride()
-    if t.shape != (rows, heads, p.d) or _dtype(t, where) != p.code or st[2] != 1 or (heads > 1 and st[1] != p.d):
+    if t.shape != shape or t.dtype is not p.dt or st[2] != 1 or (st[1] != p.d and shape[1] > 1):
         _refuse(where, "rows are [rows, heads, d] of the cache's type and sizes, a row's heads contiguous")
     return st[0]
 
@@ -581,13 +586,13 @@ def paged_append(params, K_new, V_new, Kp, Vp, table, lens, ws, cu=None, rotary=
     rows cu[b] .. cu[b+1]-1 at its last positions (cu None: row b at lens[b] - 1).  With `rotary`
     the keys are rotated on the way and Q [T, H, d] into Qo."""
     where, p, T = "fs_paged_append", params, K_new.shape[0]
-    ks, vs = _rows(p, where, K_new, p.Hkv, T), _rows(p, where, V_new, p.Hkv, T)
+    kv, q = (T, p.Hkv, p.d), (T, p.H, p.d)
+    ks, vs = _rows(p, where, K_new, kv), _rows(p, where, V_new, kv)
     _pools(p, where, Kp, Vp)
-    _table(p, where, table)
-    _ints(where, p.B, lens)
+    _table(p, where, table, lens)
     ts, qs, qos = [K_new, V_new, Kp, Vp, table, lens, ws], 0, 0
     if Q is not None and Qo is not None:
-        qs, qos = _rows(p, where, Q, p.H, T), _rows(p, where, Qo, p.H, T)
+        qs, qos = _rows(p, where, Q, q), _rows(p, where, Qo, q)
         ts += [Q, Qo]
     elif Q is not None or Qo is not None:
         _refuse(where, "Q and Qo come together")
@@ -603,10 +608,9 @@ def paged_attend(params, Q, Kp, Vp, table, lens, O, ws, lse=None, window=-1, sca
     """O [B, H, d] = attention of each sequence's newest token, query row Q[b], over its pages: all
     of them, or the last window + 1 tokens.  scale None: 1/sqrt(d).  lse: optional float32 [B, H]."""
     where, p = "fs_paged_attend", params
-    qs, os_ = _rows(p, where, Q, p.H, p.B), _rows(p, where, O, p.H, p.B)
+    qs, os_ = _rows(p, where, Q, p.row_shape), _rows(p, where, O, p.row_shape)
     _pools(p, where, Kp, Vp)
-    _table(p, where, table)
-    _ints(where, p.B, lens)
+    _table(p, where, table, lens)
     ts = [Q, Kp, Vp, table, lens, O, ws]
     if lse is not None:
         if _dtype(lse, where) != FS_F32 or lse.shape != (p.B, p.H) or not lse.is_contiguous():
@@ -620,9 +624,9 @@ def paged_attend(params, Q, Kp, Vp, table, lens, O, ws, lse=None, window=-1, sca
 def pages_reserve(params, n_new, refs, table, lens, ws, stream=None):
     """Room for n_new[b] (int32) more tokens of every sequence; lens grows by them."""
     where, p = "fs_pages_reserve", params
-    _ints(where, p.B, n_new, lens)
+    _ints(where, p.B, n_new)
     _ints(where, p.num_pages, refs)
-    _table(p, where, table)
+    _table(p, where, table, lens)
     _run(load().fs_pages_reserve, where, stream, (n_new, refs, table, lens, ws), p.c, n_new.data_ptr(), refs.data_ptr(),
          table.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.nbytes)
 
@@ -642,8 +646,7 @@ def pages_fork(params, Kp, Vp, refs, table, lens, src, dst, ws, stream=None):
     where, p, n = "fs_pages_fork", params, src.numel()
     _pools(p, where, Kp, Vp)
     _ints(where, p.num_pages, refs)
-    _table(p, where, table)
-    _ints(where, p.B, lens)
+    _table(p, where, table, lens)
     _ints(where, n, src, dst)
     _run(load().fs_pages_fork, where, stream, (Kp, Vp, refs, table, lens, src, dst, ws), p.c, Kp.data_ptr(),
          Vp.data_ptr(), refs.data_ptr(), table.data_ptr(), lens.data_ptr(), src.data_ptr(), dst.data_ptr(), n,
@@ -654,8 +657,7 @@ def pages_free(params, refs, table, lens, rows, ws, stream=None):
     """The sequences rows[i] (int32) give their pages back and are empty."""
     where, p, n = "fs_pages_free", params, rows.numel()
     _ints(where, p.num_pages, refs)
-    _table(p, where, table)
-    _ints(where, p.B, lens)
+    _table(p, where, table, lens)
     _ints(where, n, rows)
     _run(load().fs_pages_free, where, stream, (refs, table, lens, rows, ws), p.c, refs.data_ptr(), table.data_ptr(),
          lens.data_ptr(), rows.data_ptr(), n, ws.data_ptr(), ws.nbytes)
