@@ -20,10 +20,10 @@ struct AppendArgs {
     int *flag;
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_constant__ AppendArgs A, const T *Q, T *Qo,
+__global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid_constant__ AppendArgs A, const T *Q, T *Qo,
                                                                 const T *__restrict__ Kn, const T *__restrict__ Vn,
                                                                 T *Kp, T *Vp) {
     using Unit = RowUnit<T, VE, HALF>;
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
     const int lt = threadIdx.x / A.units, u = threadIdx.x - lt * A.units;
     const int t0 = blockIdx.x * per, t = t0 + lt;
 
-    // the sequence of the block's first token: the interval of cu that holds it, cut into 256
+    // the sequence of the block's first token: the interval of cu that holds it, cut into 128
     // parts at a time, each thread testing one
     int b = t;
     if (A.cu) {

@@ -27,10 +27,10 @@ struct RopeArgs {
     const int32_t *pos;
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_constant__ RopeArgs A,
+__global__ void __launch_bounds__(kRopeThreads, 10) rope_kernel(const __grid_constant__ RopeArgs A,
                                                             const T *Q, T *Qo, const T *K, T *Ko) {
     using Unit = RowUnit<T, VE, HALF>;
     constexpr int kRopeAhead = HALF ? 2 : 4;   // heads in flight per thread: four vectors either way

@@ -351,12 +351,13 @@ def same_book(book, refs, table, lens):
     assert refs.tolist() == book.refs and table.tolist() == book.table and lens.tolist() == book.lens
 
 
-@pytest.mark.parametrize("pages,page", [(64, 16), (20000, 4)])
-def test_reserve_fork_free_compact_against_the_book(pages, page):
+@pytest.mark.parametrize("pages,page,B", [(64, 16, 24), (20000, 4, 24), (4000, 2, 1300)])
+def test_reserve_fork_free_compact_against_the_book(pages, page, B):
     """Random calls; tables, counts and lengths equal the book's after each, the pools' moved
-    tokens too, and a refused call changes nothing."""
+    tokens too, and a refused call changes nothing.  Fewer pages and sequences than a block looks
+    at in a step, and more."""
     rng = np.random.default_rng(pages)
-    B, width = 24, max(16, pages // 8)
+    width = max(16, pages // 8)
     p = fs.PagedParams(B=B, H=2, Hkv=2, page_size=page, num_pages=pages, max_pages=width, dtype="f32")
     K, V, refs, table, lens = fs.alloc_pages(p)
     ws = fs.alloc_paged_workspace(p)
@@ -384,7 +385,7 @@ def test_reserve_fork_free_compact_against_the_book(pages, page):
             for a, b, n in moved or []:
                 K0[b, :, :n] = K0[a, :, :n]
         elif what == "free":
-            rows = rng.integers(0, B, rng.integers(1, 10)).tolist()          # the same one twice now and then
+            rows = rng.integers(0, B, rng.integers(1, max(10, B // 2))).tolist()     # the same one twice now and then
             book.free(rows)
             fs.pages_free(p, refs, table, lens, ints(rows), ws)
         else:
