@@ -377,9 +377,9 @@ fs_status fs_rope_backward(const fs_rope_params *p, const fs_rotary *rot, const 
  * that the caller owns; a new cache has table = -1, lens = 0, refs = 0.
  *
  * Supported: d = 64, 128 or 256; H a multiple of Hkv; any page_size >= 1 with
- * max_pages page_size < 2^30; num_pages <= 2,000,000; strides that are multiples of 16 bytes and
- * keep the elements of a pool apart (pools of any size: offsets are 64-bit); dtype bf16, f16 or
- * f32.
+ * max_pages page_size < 2^30; num_pages <= 2,000,000; H <= 65535; Hkv page_size d <= 2^30;
+ * strides that are multiples of 16 bytes and keep the elements of a pool apart (pools of any
+ * size: offsets are 64-bit); dtype bf16, f16 or f32.
  *
  * ws: fs_paged_workspace_size bytes of device workspace, zero-filled once; its first bytes hold
  * the device error flag read by fs_sync_status.  Calls that share a workspace must be ordered

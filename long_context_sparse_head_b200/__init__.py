@@ -167,7 +167,7 @@ class Params:
         c.alpha = self.alpha.ctypes.data_as(fp)
         c.lambda_ = self.lam.ctypes.data_as(fp) if self.lam is not None else fp()
         c.sigma = self.sigma.ctypes.data_as(fp) if self.sigma is not None else fp()
-        c.dtype = FS_BF16 if dtype == "bf16" else FS_F32
+        c.dtype = {"bf16": FS_BF16, "f16": FS_F16}.get(dtype, FS_F32)     # f16: refused by these calls
         self.c = c
         self.B, self.H, self.Nq, self.Nk, self.d, self.s, self.K = B, H, Nq, Nk, d, s, K
         self.dtype = dtype

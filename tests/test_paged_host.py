@@ -197,6 +197,12 @@ def test_binding_checks_its_tensors():
         assert e.value.code == 1, i
 
 
+def test_the_forward_pass_refuses_f16():
+    with pytest.raises(fs.FsError) as e:
+        fs.workspace_size(fs.Params(B=1, H=2, Nq=256, Nk=256, alpha=[0.5, 1.0], dtype="f16"))
+    assert e.value.code == 1
+
+
 def test_position_to_page_arithmetic():
     """The division by a reciprocal that the kernels use, at every page size's borders."""
     for page in list(range(1, 300)) + [511, 512, 513, 4095, 65535, 65536, 65537, (1 << 29) - 1, (1 << 30) - 1]:
