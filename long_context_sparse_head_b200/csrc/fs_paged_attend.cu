@@ -841,21 +841,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
             // then their results: one CTA reads n results no faster than one after the other.
             // Counters: of a group by its first CTA, of rows that begin there and of rows that
             // go on there apart; of the groups by the row's first CTA.
-            if (n <= kFlatJoin) {
-                if (last(A.count + c0, n)) join(0, 1, n, nullptr);
-            } else {
-                int size = kFlatJoin / 2;
-                while (size * size < n) size++;
-                const int first = ((int)blockIdx.x - c0) / size * size;        // of the CTA's group
-                const int count = min(size, n - first);
-                if (last(A.count + (first ? kMaxGrid : 0) + c0 + first, count)) {
-                    join(first, 1, count, part_of(first));
-                    const int groups = (n + size - 1) / size;
-                    if (last(A.count + 2 * kMaxGrid + c0, groups)) {
-                        __syncthreads();
-                        join(0, size, groups, nullptr);
-                    }
-                }
+            int size = n;
+            if (n > kFlatJoin)
+                for (size = kFlatJoin / 2; size * size < n;) size++;
+            int i0 = ((int)blockIdx.x - c0) / size * size, step = 1, count = min(size, n - i0);
+            int *counter = A.count + (i0 ? kMaxGrid : 0) + c0 + i0;
+            while (last(counter, count)) {
+                const bool out = step > 1 || size == n;
+                join(i0, step, count, out ? nullptr : part_of(i0));
+                if (out) break;
+                i0 = 0;
+                step = size;
+                count = (n + size - 1) / size;
+                counter = A.count + 2 * kMaxGrid + c0;
             }
         }
         __syncthreads();                       // the results, s_m and s_l are free again
