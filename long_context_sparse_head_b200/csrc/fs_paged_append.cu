@@ -23,9 +23,8 @@ struct AppendArgs {
 constexpr int kAppendThreads = 128;
 
 template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid_constant__ AppendArgs A, const T *Q, T *Qo,
-                                                                const T *__restrict__ Kn, const T *__restrict__ Vn,
-                                                                T *Kp, T *Vp) {
+__global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid_constant__ AppendArgs A, const T *Q,
+                                                                    T *Qo, const T *Kn, const T *Vn, T *Kp, T *Vp) {
     using Unit = RowUnit<T, VE, HALF>;
     constexpr int kAhead = HALF ? 2 : 4;       // rows in flight per thread: four vectors either way
     __shared__ int s_lo, s_hi;
@@ -39,7 +38,7 @@ __global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid
     // parts at a time, each thread testing one
     int b = t;
     if (A.cu) {
-        const int total = __ldg(A.cu + P.B);
+        const int total = A.cu[P.B];
         if (t0 >= total) return;               // padding, the whole block
         if (threadIdx.x == 0) {
             s_lo = 0;
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid
             const long long a = lo + (long long)threadIdx.x * step;
             if (a < hi) {
                 const int e = (int)min(a + step, (long long)hi);
-                if (__ldg(A.cu + a) <= t0 && t0 < __ldg(A.cu + e)) {
+                if (A.cu[a] <= t0 && t0 < A.cu[e]) {
                     s_lo = (int)a;
                     s_hi = e;
                 }
@@ -66,13 +65,13 @@ __global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid
             hi = nhi;
         }
         b = lo;
-        while (t < total && b + 1 < P.B && t >= __ldg(A.cu + b + 1)) b++;
+        while (t < total && b + 1 < P.B && t >= A.cu[b + 1]) b++;
     }
     if (lt >= per || t >= A.T) return;
 
-    int len = __ldg(A.lens + b), pos = len - 1;
+    int len = A.lens[b], pos = len - 1;
     if (A.cu) {
-        const int c0 = __ldg(A.cu + b), c1 = __ldg(A.cu + b + 1);
+        const int c0 = A.cu[b], c1 = A.cu[b + 1];
         if (t < c0 || t >= c1) return;         // padding
         pos = (int)max((long long)len - c1 + t, -1ll);
     } else if (len == 0) {
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid
     }
     int pi, slot;
     P.locate(pos, pi, slot);
-    const int page = __ldg(A.table + (long long)b * P.max_pages + pi);
+    const int page = A.table[(long long)b * P.max_pages + pi];
     if (!P.page_ok(page)) {
         raise_check(A.flag);
         return;

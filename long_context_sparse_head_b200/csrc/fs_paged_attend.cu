@@ -135,7 +135,7 @@ template <int KEYS> struct Rows {
         if (in) {
             int pi;
             P.locate(tok, pi, slot);
-            page = __ldg(trow + pi);
+            page = trow[pi];
         }
     }
 };
@@ -176,7 +176,7 @@ template <typename T, int D, int HT> struct TcState {
         if constexpr (kQShared) {              // 16-byte column c of head h at column c ^ (h & 7)
             for (int x = threadIdx.x; x < HT * D / 8; x += kThreads) {
                 const int h = x / (D / 8), c = x % (D / 8);
-                sq[h * (D / 8) + (c ^ (h & 7))] = h < heads ? __ldg(reinterpret_cast<const uint4 *>(Q) + x) : make_uint4(0, 0, 0, 0);
+                sq[h * (D / 8) + (c ^ (h & 7))] = h < heads ? *(reinterpret_cast<const uint4 *>(Q) + x) : make_uint4(0, 0, 0, 0);
             }
             __syncthreads();
         }
@@ -188,7 +188,7 @@ template <typename T, int D, int HT> struct TcState {
 #pragma unroll
                 for (int t = 0; t < DT; t++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) q[n][t][e] = h < heads ? __ldg(row + 8 * t + 4 * e + lane % 4) : 0u;
+                    for (int e = 0; e < 2; e++) q[n][t][e] = h < heads ? *(row + 8 * t + 4 * e + lane % 4) : 0u;
             }
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
@@ -538,7 +538,7 @@ __device__ __forceinline__ void add4(float4 &a, float f, const float4 &b) {
 
 // Tokens [first, n) that sequence b attends to.
 __device__ __forceinline__ void span(const AttendArgs &A, int b, int &first, int &n) {
-    n = __ldg(A.lens + b);
+    n = A.lens[b];
     if (n < 0 || n > A.P.cap) {
         raise_check(A.flag);
         n = n < 0 ? 0 : A.P.cap;
@@ -596,8 +596,7 @@ template <int KEYS> __device__ __forceinline__ int chunks_of(const Segment &s, i
 
 template <typename T, int D, int HT>
 __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
-    paged_attend_kernel(const __grid_constant__ AttendArgs A, const T *__restrict__ Q, const T *__restrict__ Kp,
-                        const T *__restrict__ Vp, T *__restrict__ O, float *__restrict__ lse) {
+    paged_attend_kernel(const __grid_constant__ AttendArgs A, const T *Q, const T *Kp, const T *Vp, T *O, float *lse) {
     using S = Shape<T, D, HT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[kWarps][HT], s_l[kWarps][HT], s_fac[HT][33];
@@ -658,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
         const int units = units_at(at.b);
         at.r = (int)(s_rem / units);
         at.unit = (int)(s_rem - (long long)at.r * units);
-        at.left = (int)(end - begin);          // <= 2^31 for any batch that fits a GPU's memory
+        at.left = (int)(end - begin);          // fits: checked at the call
     }
 
     // The warp's ring of stages runs on over the rows: `ahead` is the segment whose chunks are

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kRopeThreads, 10) rope_kernel(const __grid_con
     const int b = t / A.N, n = t - b * A.N;
     float c[Unit::kPairs], s[Unit::kPairs];
     if (u < A.nrot) {
-        const long long pos = A.pos ? (long long)__ldg(A.pos + b * A.pos_b + n) : A.pos0 + n;
+        const long long pos = A.pos ? (long long)A.pos[b * A.pos_b + n] : A.pos0 + n;
 #pragma unroll
         for (int m = 0; m < Unit::kPairs; m++)
             rotary_angle(A.rot.turns[Unit::pair(u, m)], pos, A.rot.mscale, A.sign, c[m], s[m]);
