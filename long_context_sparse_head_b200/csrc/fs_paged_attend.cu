@@ -33,7 +33,8 @@ namespace fs {
 namespace {
 
 constexpr int kSms = 148, kMaxGrid = 3 * kSms;   // three CTAs per SM at most
-constexpr int kFlatJoin = 16;                   // results that one CTA joins at once
+constexpr int kFlatJoin = 16;                   // most results that one CTA joins in one step
+constexpr int kDeep = 4;                        // results in flight in a join
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -812,11 +813,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
                     const int y = x + kThreads < items ? x + kThreads : x;
                     const int hx = x / (D / 4), hy = y / (D / 4);
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-#pragma unroll 8
-                    for (int i = 0; i < count; i++) {
-                        const float4 *p = reinterpret_cast<const float4 *>(part_of(i0 + i * step));
-                        add4(a, s_fac[hx][i], __ldcg(p + x));
-                        add4(b, s_fac[hy][i], __ldcg(p + y));
+                    // kDeep results in flight at a time; past the last, its again with the factor 0
+                    for (int i = 0; i < count; i += kDeep) {
+                        float4 u[kDeep], v[kDeep];
+#pragma unroll
+                        for (int j = 0; j < kDeep; j++) {
+                            const float4 *p = reinterpret_cast<const float4 *>(part_of(i0 + min(i + j, count - 1) * step));
+                            u[j] = __ldcg(p + x);
+                            v[j] = __ldcg(p + y);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kDeep; j++) {
+                            add4(a, s_fac[hx][i + j], u[j]);
+                            add4(b, s_fac[hy][i + j], v[j]);
+                        }
                     }
                     auto put = [&](int z, int h, const float4 &v) {
                         const int c = z % (D / 4) * 4;
