@@ -412,14 +412,18 @@ def _dtype(t, where):
     return code
 
 
-def _run(fn, where, stream, tensors, *args):
-    """fn(*args, stream) with the tensors' device current; on that device's current stream unless given."""
+def _one_device(where, *tensors):
     dev = tensors[0].get_device()
     if dev < 0:
         _refuse(where, "tensors are on a CUDA device")
     for t in tensors:
         if t.get_device() != dev:
             _refuse(where, "all tensors are on one device")
+    return dev
+
+
+def _call(fn, where, dev, stream, *args):
+    """fn(*args, stream) with device dev current; on that device's current stream unless given."""
     if _torch is None:
         _types()
     stream = _raw_stream(dev) if stream is None else _stream(stream)
@@ -430,6 +434,10 @@ def _run(fn, where, stream, tensors, *args):
             code = fn(*args, stream)
     if code:
         raise FsError(code, where)
+
+
+def _run(fn, where, stream, tensors, *args):
+    _call(fn, where, _one_device(where, *tensors), stream, *args)
 
 
 # ---- rotary positions ----------------------------------------------------------------
@@ -474,10 +482,11 @@ def _rope(fn, where, rotary, Q, Qo, K, Ko, positions, pos0, stream):
     if positions is not None:
         if positions.dtype is not (_torch or _types()).int32:
             _refuse(where, "positions are int32")
-        if positions.shape not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
+        st = positions.stride()
+        if positions.shape not in ((B, N), (N,)) or (N > 1 and st[-1] != 1):
             _refuse(where, "positions are [N] or [B,N], a row contiguous")
-        if positions.dim() == 2:
-            ps = positions.stride(0)
+        if len(st) == 2:
+            ps = st[0]
         ts.append(positions)
     c = FsRopeParams(B, N, H, Hk, d, qs[0], qs[1], qs[2], qos[0], qos[1], qos[2], ks_[0], ks_[1], ks_[2], kos[0], kos[1],
                      kos[2], _dtype(Q, where))
@@ -586,39 +595,60 @@ def paged_append(params, K_new, V_new, Kp, Vp, table, lens, ws, cu=None, rotary=
     rows cu[b] .. cu[b+1]-1 at its last positions (cu None: row b at lens[b] - 1).  With `rotary`
     the keys are rotated on the way and Q [T, H, d] into Qo."""
     where, p, T = "fs_paged_append", params, K_new.shape[0]
-    kv, q = (T, p.Hkv, p.d), (T, p.H, p.d)
-    ks, vs = _rows(p, where, K_new, kv), _rows(p, where, V_new, kv)
-    _pools(p, where, Kp, Vp)
+    dt, d, kv = p.dt, p.d, (T, p.Hkv, p.d)
+    ks, vs = K_new.stride(), V_new.stride()
+    if not (K_new.shape == V_new.shape == kv and Kp.shape == Vp.shape == p.shape and
+            K_new.dtype is dt and V_new.dtype is dt and Kp.dtype is dt and Vp.dtype is dt and
+            ks[1] == vs[1] == d and ks[2] == vs[2] == 1 and Kp.stride() == Vp.stride() == p.stride4):
+        _rows(p, where, K_new, kv)             # what is wrong, or a dimension of one, whose stride says nothing
+        _rows(p, where, V_new, kv)
+        _pools(p, where, Kp, Vp)
     _table(p, where, table, lens)
-    ts, qs, qos = [K_new, V_new, Kp, Vp, table, lens, ws], 0, 0
+    dev = K_new.get_device()
+    if not V_new.get_device() == Kp.get_device() == Vp.get_device() == table.get_device() == lens.get_device() == \
+            ws.get_device() == dev >= 0:
+        _one_device(where, K_new, V_new, Kp, Vp, table, lens, ws)
+    qs = qos = 0
     if Q is not None and Qo is not None:
+        q = (T, p.H, d)
         qs, qos = _rows(p, where, Q, q), _rows(p, where, Qo, q)
-        ts += [Q, Qo]
+        if not Q.get_device() == Qo.get_device() == dev:
+            _refuse(where, "all tensors are on one device")
     elif Q is not None or Qo is not None:
         _refuse(where, "Q and Qo come together")
     if cu is not None:
         _ints(where, p.B + 1, cu)
-        ts.append(cu)
-    _run(load().fs_paged_append, where, stream, ts, p.c, None if rotary is None else rotary.c, T, _ptr(Q), qs, _ptr(Qo),
-         qos, K_new.data_ptr(), ks, V_new.data_ptr(), vs, _ptr(cu), Kp.data_ptr(), Vp.data_ptr(), table.data_ptr(),
-         lens.data_ptr(), ws.data_ptr(), ws.nbytes)
+        if cu.get_device() != dev:
+            _refuse(where, "all tensors are on one device")
+    _call(load().fs_paged_append, where, dev, stream, p.c, None if rotary is None else rotary.c, T, _ptr(Q), qs, _ptr(Qo),
+          qos, K_new.data_ptr(), ks[0], V_new.data_ptr(), vs[0], _ptr(cu), Kp.data_ptr(), Vp.data_ptr(),
+          table.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
 def paged_attend(params, Q, Kp, Vp, table, lens, O, ws, lse=None, window=-1, scale=None, stream=None):
     """O [B, H, d] = attention of each sequence's newest token, query row Q[b], over its pages: all
     of them, or the last window + 1 tokens.  scale None: 1/sqrt(d).  lse: optional float32 [B, H]."""
     where, p = "fs_paged_attend", params
-    qs, os_ = _rows(p, where, Q, p.row_shape), _rows(p, where, O, p.row_shape)
-    _pools(p, where, Kp, Vp)
+    qs, os_, dt, d = Q.stride(), O.stride(), p.dt, p.d
+    if not (Q.shape == O.shape == p.row_shape and Kp.shape == Vp.shape == p.shape and
+            Q.dtype is dt and O.dtype is dt and Kp.dtype is dt and Vp.dtype is dt and
+            qs[1] == os_[1] == d and qs[2] == os_[2] == 1 and Kp.stride() == Vp.stride() == p.stride4):
+        _rows(p, where, Q, p.row_shape)        # what is wrong, or a dimension of one, whose stride says nothing
+        _rows(p, where, O, p.row_shape)
+        _pools(p, where, Kp, Vp)
     _table(p, where, table, lens)
-    ts = [Q, Kp, Vp, table, lens, O, ws]
+    dev = Q.get_device()
+    if not Kp.get_device() == Vp.get_device() == table.get_device() == lens.get_device() == O.get_device() == \
+            ws.get_device() == dev >= 0:
+        _one_device(where, Q, Kp, Vp, table, lens, O, ws)
     if lse is not None:
         if _dtype(lse, where) != FS_F32 or lse.shape != (p.B, p.H) or not lse.is_contiguous():
             _refuse(where, "lse is contiguous float32 [B, H]")
-        ts.append(lse)
-    _run(load().fs_paged_attend, where, stream, ts, p.c, Q.data_ptr(), qs, Kp.data_ptr(), Vp.data_ptr(),
-         table.data_ptr(), lens.data_ptr(), int(window), p.scale if scale is None else scale, O.data_ptr(), os_,
-         _ptr(lse), ws.data_ptr(), ws.nbytes)
+        if lse.get_device() != dev:
+            _refuse(where, "all tensors are on one device")
+    _call(load().fs_paged_attend, where, dev, stream, p.c, Q.data_ptr(), qs[0], Kp.data_ptr(), Vp.data_ptr(),
+          table.data_ptr(), lens.data_ptr(), int(window), p.scale if scale is None else scale, O.data_ptr(), os_[0],
+          _ptr(lse), ws.data_ptr(), ws.nbytes)
 
 
 def pages_reserve(params, n_new, refs, table, lens, ws, stream=None):
