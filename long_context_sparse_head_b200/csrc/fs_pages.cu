@@ -210,12 +210,54 @@ __device__ __forceinline__ void copy_slab(const PageShape &G, uint4 *pool, int s
         if (at[j] >= 0) __stcs(to + at[j], v[j]);
 }
 
-// Pages src[i] -> dst[i] of both pools, i < n.
+// The same for pages smaller than a slab: as many of them as fill it, vectors first .. first + 255
+// of the 2 n pages (K's and V's by turns) laid end to end.
+__device__ __forceinline__ void copy_small(const PagedDev &P, const PageShape &G, uint4 *Kp, uint4 *Vp,
+                                           const int32_t *src, const int32_t *dst, int n, long long first, int lane,
+                                           int *flag) {
+    const long long page0 = (first + lane) / G.vecs;
+    const int x0 = (int)(first + lane - page0 * G.vecs);
+    uint4 v[kCopyAhead], *to[kCopyAhead];
+#pragma unroll
+    for (int j = 0; j < kCopyAhead; j++) {
+        const int x = x0 + 32 * j, k = x / G.vecs;
+        const long long page = page0 + k;
+        to[j] = nullptr;
+        if (page >= 2ll * n) continue;
+        const int a = src[page >> 1], b = dst[page >> 1];
+        if (!P.page_ok(a) || !P.page_ok(b)) {
+            raise_check(flag);
+            continue;
+        }
+        uint4 *pool = page & 1 ? Vp : Kp;
+        const long long at = G.at(x - k * G.vecs);
+        to[j] = pool + b * G.sp + at;
+        v[j] = __ldcs(pool + a * G.sp + at);
+    }
+#pragma unroll
+    for (int j = 0; j < kCopyAhead; j++)
+        if (to[j]) __stcs(to[j], v[j]);
+}
+
+// Pages of fewer vectors are copied many to a slab.
+constexpr int kSmallPage = kSlab / 2;
+// Slabs that the pages src[i] -> dst[i] of both pools, i < n, make.
+__host__ __device__ __forceinline__ long long slabs_of(const PageShape &G, long long n) {
+    return G.vecs < kSmallPage ? (2 * n * G.vecs + kSlab - 1) / kSlab : 2 * n * ((G.vecs + kSlab - 1) / kSlab);
+}
+
+// Pages src[i] -> dst[i] of both pools, i < n.  Small pages share slabs (900,000 of 128 bytes: 104 us, a
+// warp each 650; 60,000 of 1 KB: 42, 54); from 2 KB on, where sharing gains nothing, a page is slabs of its own.
+template <bool SMALL>
 __device__ __forceinline__ void copy_pages(const PagedDev &P, const PageShape &G, uint4 *Kp, uint4 *Vp,
                                            const int32_t *src, const int32_t *dst, int n, int *flag) {
     const int lane = threadIdx.x & 31, slabs = (G.vecs + kSlab - 1) / kSlab;
-    const long long tasks = 2ll * n * slabs, stride = (long long)gridDim.x * (kCopyThreads / 32);
+    const long long tasks = slabs_of(G, n), stride = (long long)gridDim.x * (kCopyThreads / 32);
     for (long long t = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); t < tasks; t += stride) {
+        if constexpr (SMALL) {
+            copy_small(P, G, Kp, Vp, src, dst, n, t * kSlab, lane, flag);
+            continue;
+        }
         const long long pair = t / slabs;
         const int slab = (int)(t - pair * slabs), i = (int)(pair >> 1);
         const int a = src[i], b = dst[i];
@@ -227,11 +269,12 @@ __device__ __forceinline__ void copy_pages(const PagedDev &P, const PageShape &G
     }
 }
 
+template <bool SMALL>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ PagedDev P,
                                                             const __grid_constant__ PageShape G, uint4 *Kp, uint4 *Vp,
                                                             const int32_t *src, const int32_t *dst, int n, int *flag) {
     griddep_wait();
-    copy_pages(P, G, Kp, Vp, src, dst, n, flag);
+    copy_pages<SMALL>(P, G, Kp, Vp, src, dst, n, flag);
 }
 
 // Fork, first part: checks everything, finds a page for every part-filled tail, sets lens.
@@ -435,6 +478,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
 }
 
 // Packing, second part: the pages, the refs, the table.
+template <bool SMALL>
 __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const __grid_constant__ PagedDev P,
                                                                const __grid_constant__ PageShape G, uint4 *Kp, uint4 *Vp,
                                                                const int32_t *refs, const int32_t *table,
@@ -465,7 +509,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const __grid_cons
         refs_out[hole[x]] = count[x];
         if (refs_out == refs) refs_out[mover[x]] = 0;
     }
-    copy_pages(P, G, Kp, Vp, mover, hole, moves, flag);
+    copy_pages<SMALL>(P, G, Kp, Vp, mover, hole, moves, flag);
 }
 
 // ---- host side
@@ -496,7 +540,7 @@ PageShape page_shape(const PagedDev &P, fs_dtype dt) {
 }
 
 unsigned copy_grid(const PageShape &G, long long pages) {
-    const long long tasks = 2 * pages * ((G.vecs + kSlab - 1) / kSlab), warps = kCopyThreads / 32;
+    const long long tasks = slabs_of(G, pages), warps = kCopyThreads / 32;
     return (unsigned)std::max(1ll, std::min((tasks + warps - 1) / warps, 148ll * 8));
 }
 
@@ -605,7 +649,7 @@ extern "C" fs_status fs_pages_copy(const fs_paged_params *p, void *Kp, void *Vp,
     const PageShape G = page_shape(P, p->dtype);
     const cudaStream_t st = (cudaStream_t)stream;
     LaunchScope scope(kPagesCopy, st);
-    return done(launch_pdl(copy_kernel, dim3(copy_grid(G, n)), dim3(kCopyThreads), 0, st, P, G, (uint4 *)Kp, (uint4 *)Vp,
+    return done(launch_pdl(G.vecs < kSmallPage ? copy_kernel<true> : copy_kernel<false>, dim3(copy_grid(G, n)), dim3(kCopyThreads), 0, st, P, G, (uint4 *)Kp, (uint4 *)Vp,
                            src, dst, n, static_cast<int *>(ws)));
 }
 
@@ -669,6 +713,6 @@ extern "C" fs_status fs_pages_compact(const fs_paged_params *p, void *Kp, void *
     const unsigned grid = (unsigned)std::max<long long>(copy_grid(G, P.num_pages),
                                                         std::min((rows + kCopyThreads - 1) / kCopyThreads, 148ll * 8));
     LaunchScope scope(kPagesCompact, st);
-    return done(launch_pdl(compact_kernel, dim3(grid), dim3(kCopyThreads), 0, st, P, G, (uint4 *)Kp, (uint4 *)Vp, refs,
+    return done(launch_pdl(G.vecs < kSmallPage ? compact_kernel<true> : compact_kernel<false>, dim3(grid), dim3(kCopyThreads), 0, st, P, G, (uint4 *)Kp, (uint4 *)Vp, refs,
                            table, refs_out, table_out, (const int *)area_of(ws), static_cast<int *>(ws)));
 }
