@@ -177,7 +177,8 @@ template <typename T, int D, int HT> struct TcState {
         if constexpr (kQShared) {              // 16-byte column c of head h at column c ^ (h & 7)
             for (int x = threadIdx.x; x < HT * D / 8; x += kThreads) {
                 const int h = x / (D / 8), c = x % (D / 8);
-                sq[h * (D / 8) + (c ^ (h & 7))] = h < heads ? *(reinterpret_cast<const uint4 *>(Q) + x) : make_uint4(0, 0, 0, 0);
+                sq[h * (D / 8) + (c ^ (h & 7))] =
+                    h < heads ? reinterpret_cast<const uint4 *>(Q)[x] : make_uint4(0, 0, 0, 0);
             }
             __syncthreads();
         }
@@ -189,7 +190,7 @@ template <typename T, int D, int HT> struct TcState {
 #pragma unroll
                 for (int t = 0; t < DT; t++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) q[n][t][e] = h < heads ? *(row + 8 * t + 4 * e + lane % 4) : 0u;
+                    for (int e = 0; e < 2; e++) q[n][t][e] = h < heads ? row[8 * t + 4 * e + lane % 4] : 0u;
             }
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
@@ -682,9 +683,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
             // its query rows, to L2: they are read when the row is begun
             const int h0 = ahead.hkv * A.G + (ahead.r - ahead.hkv * A.NG) * HT;
             if (warp == 0 && lane * (128 / (int)sizeof(T)) < min(HT, (ahead.hkv + 1) * A.G - h0) * D)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(Q + ahead.b * A.qs + h0 * D + lane * (128 / (int)sizeof(T))));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(Q + ahead.b * A.qs + h0 * D +
+                                                              lane * (128 / (int)sizeof(T))));
         }
-        rows.find(P, A.table + (long long)ahead.b * P.max_pages, ahead.t0 + (warp + kWarps * next) * S::kKeys, ahead.t1, lane);
+        rows.find(P, A.table + (long long)ahead.b * P.max_pages, ahead.t0 + (warp + kWarps * next) * S::kKeys, ahead.t1,
+                  lane);
         next++;
     };
     auto fill = [&](int slot) {
@@ -766,7 +769,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
         }
         if (!whole) {
             const long long row0 = done - g.unit;                              // the row's first unit among all
-            const int c0 = (int)((row0 + kRowCost) / per), n = (int)((row0 + g.units - 1) / per) - c0 + 1;   // its CTAs
+            const int c0 = (int)((row0 + kRowCost) / per);                     // its CTAs
+            const int n = (int)((row0 + g.units - 1) / per) - c0 + 1;
             // c0's result of the row is its second (the row begins there), the others' their first
             auto part_of = [&](int i) { return A.part + ((long long)(c0 + i) * 2 + (i == 0)) * S::kPart; };
             // whether this CTA is the last of `count` to arrive
@@ -775,7 +779,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, HT>::kBlocks))
                 if (tid == 0) {
                     // releases what the block wrote before the barrier, acquires what those before it did
                     int before;
-                    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+                    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                                 : "=r"(before) : "l"(counter) : "memory");
                     s_last = before == count - 1;
                     if (s_last) *counter = 0;                                  // for the next call
                 }

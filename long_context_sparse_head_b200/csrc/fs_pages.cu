@@ -76,7 +76,8 @@ struct Cluster {
         all = 0;
         for (int r = 0; r < size; r++) {
             int x;
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(tc::cluster_map(tc::smem_u32(mine), r)) : "memory");
+            const uint32_t from = tc::cluster_map(tc::smem_u32(mine), r);
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
             if (r < rank) before += x;
             all += x;
         }
