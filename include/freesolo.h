@@ -422,9 +422,9 @@ fs_status fs_paged_append(const fs_paged_params *p, const fs_rotary *rot, int T,
  * eq. (3).  lens[b] = 0: O = 0 and lse = -inf.  A sequence with a bad entry or length (flagged)
  * has undefined outputs.
  * bf16, f16: products on the tensor cores, fp32 softmax and sums, the probabilities in two parts
- * of the type for the product with V (2^-16 of them is lost); f32: fp32 throughout.  What pages
- * hold behind the last token is never used, NaN included; an infinite value of V that is seen
- * makes its outputs infinite or NaN. */
+ * of the type for the product with V (at most 2^-16 of each is lost; f16: or 2^-40 of the largest
+ * one); f32: fp32 throughout.  What pages hold behind the last token is never used, NaN included;
+ * an infinite value of V that is seen makes its outputs infinite or NaN. */
 fs_status fs_paged_attend(const fs_paged_params *p, const void *Q, long long q_stride, const void *Kp, const void *Vp,
                           const int32_t *table, const int32_t *lens, int window, float scale, void *O,
                           long long o_stride, float *lse, void *ws, size_t ws_bytes, void *stream);

@@ -80,6 +80,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 template <typename T> struct Half2;
 template <> struct Half2<__nv_bfloat16> {
+    static constexpr float kRaise = 1.f, kLower = 1.f;
     __device__ __forceinline__ static uint32_t pack(float a, float b) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&v);
@@ -92,6 +93,10 @@ template <> struct Half2<__nv_bfloat16> {
     }
 };
 template <> struct Half2<__half> {
+    // Probabilities (at most 1) are raised by 2^15 for the product with V, which still fits under 65504,
+    // and the accumulators lowered at the row's end: f16 ends at steps of 2^-24, so that unraised a
+    // probability of 2^-16 would lose 2^-9 of itself and one below 2^-25 be gone, while the sum counts it.
+    static constexpr float kRaise = 0x1p15f, kLower = 0x1p-15f;
     __device__ __forceinline__ static uint32_t pack(float a, float b) {
         const __half2 v = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&v);
@@ -272,9 +277,10 @@ template <typename T, int D, int HT> struct TcState {
                     for (int e = 0; e < 4; e++) o[t][n][e] *= f[n][e & 1];
         }
         // For the product with V a probability goes in two parts, T's nearest value and what is left,
-        // rounded to T: 2^-16 of it is lost at most, where one part alone adds as much error as the
-        // output's own rounding (262144 tokens in bf16: 2.2e-3 of the output, 1.6e-3 with both).  The
-        // second product costs up to 3% at 16 heads a group, nothing where HBM bounds it.
+        // rounded to T: 2^-16 of it is lost at most (f16: or 2^-40 of the largest, where the second part
+        // ends), where one part alone adds as much error as the output's own rounding (262144 tokens
+        // in bf16: 2.2e-3 of the output, 1.6e-3 with both).  The second product costs up to 3% at 16
+        // heads a group, nothing where HBM bounds it.
         const uint32_t vbase = stage + S::kKeys * S::kRowBytes;
 #pragma unroll
         for (int i = 0; i < MT; i++) {
@@ -283,7 +289,7 @@ template <typename T, int D, int HT> struct TcState {
             for (int n = 0; n < NT; n++)
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
-                    const float x = s[i][n][2 * k], y = s[i][n][2 * k + 1];
+                    const float x = s[i][n][2 * k] * Half2<T>::kRaise, y = s[i][n][2 * k + 1] * Half2<T>::kRaise;
                     const uint32_t near = Half2<T>::pack(x, y);
                     const float2 z = Two<T>::get(near);
                     p[0][n][k] = transpose8(near);
@@ -321,8 +327,8 @@ template <typename T, int D, int HT> struct TcState {
                 }
 #pragma unroll
                 for (int t = 0; t < DT; t++) {
-                    out[S::out(h, 16 * t + lane / 4)] = o[t][n][e];
-                    out[S::out(h, 16 * t + lane / 4 + 8)] = o[t][n][e + 2];
+                    out[S::out(h, 16 * t + lane / 4)] = o[t][n][e] * Half2<T>::kLower;
+                    out[S::out(h, 16 * t + lane / 4 + 8)] = o[t][n][e + 2] * Half2<T>::kLower;
                 }
             }
     }

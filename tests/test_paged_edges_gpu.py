@@ -1,0 +1,58 @@
+"""Calls at the borders of what the paged cache's documentation allows, on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import long_context_sparse_head_b200 as fs
+from tests._paged import DTYPES, HALF_STEP, attend
+
+pytestmark = pytest.mark.gpu
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------- attention
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 11), (256, 16)])
+@pytest.mark.parametrize("gap", [8.0, 12.0, 15.7, 17.5, 20.0])
+def test_attend_weighs_a_long_tail_under_one_peak(dtype, d, group, gap):
+    """One key `gap` above all others, its value 0: the output is what the others' small
+    probabilities add up to.  So many sequences that no row is cut: the peak's warp holds a quarter
+    of the tail."""
+    n, B, page = 2048, 300, 32
+    p = fs.PagedParams(B=B, H=2 * group, Hkv=2, d=d, page_size=page, num_pages=3 * n // page, max_pages=n // page,
+                       dtype=dtype)
+    K, V, _, table, lens = fs.alloc_pages(p)
+    ws = fs.alloc_paged_workspace(p)
+    K.zero_()
+    V.copy_(torch.rand(p.shape, generator=torch.Generator().manual_seed(d)) + 0.5)
+    lens.fill_(n)
+    scale = d ** -0.5
+    at = (0, 1000, n - 1)                                    # the peak's place: three kinds of sequence share the pages
+    for i, t in enumerate(at):
+        pages = np.arange(i * (n // page), (i + 1) * (n // page))
+        K[int(pages[t // page]), :, t % page, 0] = gap / scale
+        V[int(pages[t // page]), :, t % page] = 0
+        table[i::3] = ints(pages)
+    q = torch.zeros((B, 2 * group, d), dtype=DTYPES[dtype], device="cuda")
+    q[..., 0] = 1
+    o, lse = torch.empty_like(q), torch.empty((B, 2 * group), device="cuda")
+    fs.paged_attend(p, q, K, V, table, lens, o, ws, lse=lse)
+    fs.sync_status(ws)
+    for i in range(3):
+        for h in range(2):
+            k, v = (f64(x[i * (n // page):(i + 1) * (n // page), h].flatten(0, 1)) for x in (K, V))
+            want, l, _ = attend(f64(q[i, :1]), k, v, scale)
+            # scores have one term: its rounding, the factor's and the exponent's, 2^-22 of the gap in
+            # all, and 2^-20 for the exponential; n sums of 2^-23; a probability's two parts lose 2^-16
+            # of it, in f16 or 2^-40 of the largest; the output's own rounding
+            rel = 2 * (gap * 2.0 ** -22 + 2.0 ** -20) + n * 2.0 ** -23 + (0.0 if dtype == "f32" else 2.0 ** -16)
+            bound = np.abs(want) * (rel + HALF_STEP[dtype]) + (n * 2.0 ** -40 * 1.5 + 2.0 ** -25 if dtype == "f16" else 0.0)
+            assert (np.abs(f64(o[i::3, h * group:(h + 1) * group]) - want) <= bound).all(), (i, h)
+            assert (np.abs(f64(lse[i::3, h * group:(h + 1) * group]) - l) <= rel + gap * 2.0 ** -22).all()
