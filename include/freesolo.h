@@ -353,8 +353,8 @@ typedef struct {
     fs_dtype dtype;           /* FS_BF16, FS_F16 or FS_F32 */
 } fs_rope_params;
 
-/* Rotates Q [B,H,N,d] into Qo and K [B,Hk,N,d] into Ko (any strides; outputs whose strides fold
- * elements together are FS_ERR_INVALID_ARG).  An output may be its own input with the same
+/* Rotates Q [B,H,N,d] into Qo and K [B,Hk,N,d] into Ko (any strides; an output whose strides fold
+ * elements together, by size one below what those before it span, is FS_ERR_INVALID_ARG).  An output may be its own input with the same
  * strides, but may not overlap it otherwise.  pos: device int32, token (b, n) at
  * pos[b pos_stride + n] (pos_stride 0: shared by the rows); NULL: position pos0 + n.  Rows that
  * start on 16-byte boundaries and whose parts are whole 16-byte vectors are moved in vectors,

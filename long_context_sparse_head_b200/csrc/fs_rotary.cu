@@ -10,7 +10,9 @@
 // through `hc` of its heads, queries then keys, so the sines are computed once for all of
 // them: at one head a thread they cost more than the memory.  Four heads are loaded before
 // the first is turned.
+#include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "fs_rotary.cuh"
@@ -103,9 +105,23 @@ cudaError_t launch_rope_op(RopeArgs &A, bool half, bool vec, bool in_place, cons
                 : launch_as<T, 1, false>(A, in_place, Q, Qo, K, Ko, st);
 }
 
-// the strides of an output must keep its elements apart
-bool apart(const long long (&s)[3], int B, int H, int N) {
-    return (B == 1 || s[0] != 0) && (H == 1 || s[1] != 0) && (N == 1 || s[2] != 0);
+// The strides of an output must keep its elements apart: taken by size, each reaches past
+// everything that the smaller ones span.
+bool apart(const long long (&s)[3], int B, int H, int N, int d) {
+    struct { long long n, s; } dim[3] = {{B, s[0]}, {H, s[1]}, {N, s[2]}};
+    for (auto &x : dim) {
+        if (x.n == 1) x.s = 0;
+        if (x.s > (1ll << 50) / x.n || x.s < -((1ll << 50) / x.n)) return false;
+        x.s = std::abs(x.s);
+    }
+    std::sort(dim, dim + 3, [](const auto &a, const auto &b) { return a.s < b.s; });
+    long long span = d;
+    for (const auto &x : dim) {
+        if (x.n == 1) continue;
+        if (x.s < span) return false;
+        span += (x.n - 1) * x.s;
+    }
+    return true;
 }
 // every row starts on a 16-byte boundary
 bool rows_aligned(const void *p, const long long (&s)[3], int B, int H, int N, size_t es) {
@@ -126,7 +142,7 @@ fs_status rope(const fs_rope_params *p, const fs_rotary *rot, const void *Q, voi
     if (T > 0x7fffffffll || Htot > 65535) return FS_ERR_UNSUPPORTED;
     if (T == 0 || Htot == 0) return FS_OK;
     if ((p->H > 0 && (!Q || !Qo)) || (p->Hk > 0 && (!K || !Ko))) return FS_ERR_INVALID_ARG;
-    if ((p->H > 0 && !apart(p->qo, p->B, p->H, p->N)) || (p->Hk > 0 && !apart(p->ko, p->B, p->Hk, p->N)))
+    if ((p->H > 0 && !apart(p->qo, p->B, p->H, p->N, p->d)) || (p->Hk > 0 && !apart(p->ko, p->B, p->Hk, p->N, p->d)))
         return FS_ERR_INVALID_ARG;
     const size_t es = dtype_bytes(p->dtype);
     const uintptr_t em = es - 1;
