@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid
     const PagedDev &P = A.P;
     const int per = kAppendThreads / A.units;  // tokens per block
     const int lt = threadIdx.x / A.units, u = threadIdx.x - lt * A.units;
-    const int t0 = blockIdx.x * per, t = t0 + lt;
+    const int t0 = blockIdx.x * per, t = lt < A.T - t0 ? t0 + lt : A.T;      // not past 2^31
 
     // the sequence of the block's first token: the interval of cu that holds it, cut into 128
     // parts at a time, each thread testing one
@@ -138,9 +138,9 @@ cudaError_t launch_as(AppendArgs &A, const void *Q, void *Qo, const void *Kn, co
     A.hc = 32;
     while (A.hc > 1 && (long long)A.T * A.units * ((A.Htot + A.hc - 1) / A.hc) < 2ll * 148 * 2048) A.hc >>= 1;
     LaunchScope scope(kPagedAppend, st);
-    return launch_pdl(append_kernel<T, VE, HALF>, dim3((unsigned)((A.T + per - 1) / per), (A.Htot + A.hc - 1) / A.hc),
-                      dim3(kAppendThreads), 0, st, A, (const T *)Q, (T *)Qo, (const T *)Kn, (const T *)Vn, (T *)Kp,
-                      (T *)Vp);
+    const unsigned gx = (unsigned)(((long long)A.T + per - 1) / per);
+    return launch_pdl(append_kernel<T, VE, HALF>, dim3(gx, (A.Htot + A.hc - 1) / A.hc), dim3(kAppendThreads), 0, st, A,
+                      (const T *)Q, (T *)Qo, (const T *)Kn, (const T *)Vn, (T *)Kp, (T *)Vp);
 }
 
 template <typename T>

@@ -39,9 +39,9 @@ __global__ void __launch_bounds__(kRopeThreads, 10) rope_kernel(const __grid_con
     griddep_wait();
     const int per = kRopeThreads / A.units;    // tokens per block
     const int lt = threadIdx.x / A.units, u = threadIdx.x - lt * A.units;
-    const int t = blockIdx.x * per + lt;
-    if (lt >= per || t >= A.T) return;
-    const int b = t / A.N, n = t - b * A.N;
+    const int t0 = blockIdx.x * per;
+    if (lt >= per || lt >= A.T - t0) return;   // t0 + lt could pass 2^31
+    const int t = t0 + lt, b = t / A.N, n = t - b * A.N;
     float c[Unit::kPairs], s[Unit::kPairs];
     if (u < A.nrot) {
         const long long pos = A.pos ? (long long)A.pos[b * A.pos_b + n] : A.pos0 + n;
@@ -83,7 +83,7 @@ cudaError_t launch_as(RopeArgs &A, bool in_place, const void *Q, void *Qo, const
     A.nrot = Unit::rot_units(A.rot.r);
     A.units = in_place ? A.nrot : Unit::units(A.d, A.rot.r);   // in place nothing is copied
     const int per = kRopeThreads / A.units;
-    const unsigned gx = (unsigned)((A.T + per - 1) / per);
+    const unsigned gx = (unsigned)(((long long)A.T + per - 1) / per);
     // heads per thread: as many as leave two threads for every one that the GPU holds at once
     // (148 x 2048), else a head each, for latency
     A.hc = 32;

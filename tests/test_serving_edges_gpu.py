@@ -1,10 +1,10 @@
-"""Calls at the borders of what the paged cache's documentation allows, on the GPU."""
+"""Calls of the serving operators at the borders of what their documentation allows, on the GPU."""
 import numpy as np
 import pytest
 import torch
 
 import long_context_sparse_head_b200 as fs
-from tests._paged import DTYPES, HALF_STEP, attend
+from tests._paged import DTYPES, HALF_STEP, attend, rotate, rotate_bound, thetas
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,35 @@ def test_attend_weighs_a_long_tail_under_one_peak(dtype, d, group, gap):
             bound = np.abs(want) * (rel + HALF_STEP[dtype]) + (n * 2.0 ** -40 * 1.5 + 2.0 ** -25 if dtype == "f16" else 0.0)
             assert (np.abs(f64(o[i::3, h * group:(h + 1) * group]) - want) <= bound).all(), (i, h)
             assert (np.abs(f64(lse[i::3, h * group:(h + 1) * group]) - l) <= rel + gap * 2.0 ** -22).all()
+
+
+# ---------------------------------------------------------------- writing
+def test_append_with_the_most_rows():
+    """2^31 - 1 rows, of which five are tokens and the others padding."""
+    T = 2 ** 31 - 1
+    p = fs.PagedParams(B=1, H=1, Hkv=1, page_size=4, num_pages=3, max_pages=2)
+    K, V, _, table, lens = fs.alloc_pages(p)
+    ws = fs.alloc_paged_workspace(p)
+    K.fill_(7)
+    V.fill_(7)
+    table.copy_(ints([[2, 0]]))
+    lens.fill_(6)
+    k = torch.full((1, 1, 64), 3.0, dtype=torch.bfloat16, device="cuda").expand(T, 1, 64)
+    fs.paged_append(p, k, k, K, V, table, lens, ws, cu=ints([0, 5]))
+    fs.sync_status(ws)
+    for x in (K, V):
+        assert x[2, 0, :, 5].tolist() == [7, 3, 3, 3] and x[0, 0, :, 5].tolist() == [3, 3, 7, 7] and (x[1] == 7).all()
+
+
+# ---------------------------------------------------------------- rotary positions
+def test_rope_of_the_most_tokens():
+    """2^31 - 1 tokens: the last block's threads stand past the last of them."""
+    T = 2 ** 31 - 1
+    x = torch.empty((T, 2), dtype=torch.float16, device="cuda")
+    x[:, 0], x[:, 1] = 1.0, -0.5
+    a = np.broadcast_to(np.array([1.0, -0.5]), (300, 2)).copy()
+    q = x.view(1, 1, T, 2)
+    fs.rope(fs.Rotary(2), q, q)
+    for first in (0, 2 ** 30 - 150, T - 300):
+        want = rotate(a, np.arange(first, first + 300), thetas(2), "interleaved")
+        assert (np.abs(f64(x[first:first + 300]) - want) <= rotate_bound(a, want, 2, "interleaved", "f16")).all()
