@@ -135,11 +135,14 @@ cudaError_t launch_as(AppendArgs &A, const void *Q, void *Qo, const void *Kn, co
     const int per = kAppendThreads / A.units;
     // rows per thread: as many as leave two threads for every one that the GPU holds at once
     // (148 x 2048), else one each, for latency
+    // (and at most 65535 blocks for the rows of a token: the most heads make 196605 rows)
     A.hc = 32;
-    while (A.hc > 1 && (long long)A.T * A.units * ((A.Htot + A.hc - 1) / A.hc) < 2ll * 148 * 2048) A.hc >>= 1;
+    auto blocks = [&](int hc) { return (A.Htot + hc - 1) / hc; };
+    while (A.hc > 1 && (long long)A.T * A.units * blocks(A.hc) < 2ll * 148 * 2048 && blocks(A.hc / 2) <= 65535)
+        A.hc >>= 1;
     LaunchScope scope(kPagedAppend, st);
     const unsigned gx = (unsigned)(((long long)A.T + per - 1) / per);
-    return launch_pdl(append_kernel<T, VE, HALF>, dim3(gx, (A.Htot + A.hc - 1) / A.hc), dim3(kAppendThreads), 0, st, A,
+    return launch_pdl(append_kernel<T, VE, HALF>, dim3(gx, blocks(A.hc)), dim3(kAppendThreads), 0, st, A,
                       (const T *)Q, (T *)Qo, (const T *)Kn, (const T *)Vn, (T *)Kp, (T *)Vp);
 }
 

@@ -88,7 +88,6 @@ cudaError_t launch_as(RopeArgs &A, bool in_place, const void *Q, void *Qo, const
     // (148 x 2048), else a head each, for latency
     A.hc = 32;
     while (A.hc > 1 && (long long)A.T * A.units * ((A.Htot + A.hc - 1) / A.hc) < 2ll * 148 * 2048) A.hc >>= 1;
-    if (A.hc < A.Htot && (A.Htot + A.hc - 1) / A.hc > 65535) return cudaErrorInvalidValue;
     LaunchScope scope(kRope, st);
     return launch_pdl(rope_kernel<T, VE, HALF>, dim3(gx, (A.Htot + A.hc - 1) / A.hc), dim3(kRopeThreads), 0, st, A,
                       (const T *)Q, (T *)Qo, (const T *)K, (T *)Ko);

@@ -76,6 +76,27 @@ def test_append_with_the_most_rows():
         assert x[2, 0, :, 5].tolist() == [7, 3, 3, 3] and x[0, 0, :, 5].tolist() == [3, 3, 7, 7] and (x[1] == 7).all()
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_append_of_one_token_with_the_most_heads(layout):
+    """More rows for a token than a grid's second dimension counts."""
+    H = 65535
+    p = fs.PagedParams(B=1, H=H, Hkv=H, page_size=2, num_pages=1, max_pages=1)
+    K, V, _, table, lens = fs.alloc_pages(p)
+    ws = fs.alloc_paged_workspace(p)
+    table.zero_()
+    lens.fill_(2)
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn((1, H, 64), generator=g).to(torch.bfloat16).cuda() for _ in range(3))
+    qo = torch.empty_like(q)
+    fs.paged_append(p, k, v, K, V, table, lens, ws, rotary=fs.Rotary(64, layout), Q=q, Qo=qo)
+    fs.sync_status(ws)
+    for x, got in ((q[0], qo[0]), (k[0], K[0, :, 1])):
+        a = f64(x)
+        want = rotate(a, 1, thetas(64), layout)
+        assert (np.abs(f64(got) - want) <= rotate_bound(a, want, 64, layout, "bf16")).all()
+    assert torch.equal(V[0, :, 1], v[0])
+
+
 # ---------------------------------------------------------------- rotary positions
 def test_rope_of_the_most_tokens():
     """2^31 - 1 tokens: the last block's threads stand past the last of them."""
