@@ -403,7 +403,8 @@ fs_status fs_paged_workspace_size(const fs_paged_params *p, size_t *bytes);
  * cu[b] .. cu[b+1]-1 (cu: device int32 [B+1], not decreasing from cu[0] = 0) and take its last
  * positions, lens[b] - n .. lens[b] - 1: lens already counts them (fs_pages_reserve).  cu NULL:
  * one row each, T = B, and a sequence with lens[b] = 0 is skipped.  Rows from cu[B] on are
- * padding and are not read; their Qo rows are left as they were.
+ * padding and are not read; their Qo rows are left as they were.  cu[B] above T sets the flag:
+ * the T rows are written, the tokens behind them are not.
  * rot (NULL: none): the keys are rotated by their positions as they are written, and so are the
  * query rows Q [T, H, d] into Qo (Q NULL: none; Q == Qo with the same stride: in place).  The
  * rows of a token that has no place (flagged) are skipped.  Rows start on 16-byte boundaries. */

@@ -39,6 +39,8 @@ __global__ void __launch_bounds__(kAppendThreads, 10) append_kernel(const __grid
     int b = t;
     if (A.cu) {
         const int total = A.cu[P.B];
+        if (total > A.T && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+            raise_check(A.flag);               // lens counts tokens that were not given
         if (t0 >= total) return;               // padding, the whole block
         if (threadIdx.x == 0) {
             s_lo = 0;

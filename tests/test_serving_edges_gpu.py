@@ -97,6 +97,27 @@ def test_append_of_one_token_with_the_most_heads(layout):
     assert torch.equal(V[0, :, 1], v[0])
 
 
+def test_append_reports_rows_that_are_counted_but_not_given():
+    """cu counts nine tokens, the call brings five rows: those are written, and it is reported that
+    the others, which lens counts too, were not."""
+    p = fs.PagedParams(B=2, H=1, Hkv=1, page_size=4, num_pages=4, max_pages=2)
+    K, V, _, table, lens = fs.alloc_pages(p)
+    ws = fs.alloc_paged_workspace(p)
+    K.fill_(7)
+    V.fill_(7)
+    table.copy_(ints([[2, -1], [0, 3]]))
+    lens.copy_(ints([3, 6]))
+    k = torch.arange(1, 6, device="cuda").to(torch.bfloat16)[:, None, None].expand(5, 1, 64).contiguous()
+    fs.paged_append(p, k, -k, K, V, table, lens, ws, cu=ints([0, 3, 9]))
+    with pytest.raises(fs.FsError) as e:
+        fs.sync_status(ws)
+    assert e.value.code == 6
+    assert K[2, 0, :, 0].tolist() == [1, 2, 3, 7] and K[0, 0, :, 0].tolist() == [4, 5, 7, 7]
+    assert V[2, 0, :, 0].tolist() == [-1, -2, -3, 7] and V[0, 0, :, 0].tolist() == [-4, -5, 7, 7]
+    fs.paged_append(p, k, -k, K, V, table, lens, ws, cu=ints([0, 3, 5]))     # exactly as many
+    fs.sync_status(ws)
+
+
 # ---------------------------------------------------------------- rotary positions
 def test_rope_of_the_most_tokens():
     """2^31 - 1 tokens: the last block's threads stand past the last of them."""
