@@ -381,8 +381,15 @@ def cache_status(cache, stream=None):
 # ---- serving: what the calls below share ---------------------------------------------
 # A decoding step makes a few of these calls, each a few microseconds on the GPU, so the checks
 # compare whole tuples first and look closer only where those differ.
+_INT = 0x7fffffff                              # the library counts in C ints; ctypes would cut what is larger
+
+
 def _refuse(where, what):
     raise FsError(1, "%s: %s" % (where, what))
+
+
+def _too_many(where):
+    raise FsError(2, "%s: a size past 2^31 - 1" % where)
 
 
 _torch = _raw_stream = _raw_device = None
@@ -475,6 +482,8 @@ def _rope(fn, where, rotary, Q, Qo, K, Ko, positions, pos0, stream):
         ts += [K, Ko]
     elif K is not None or Ko is not None:
         _refuse(where, "K and its output come together")
+    if max(shape) > _INT or Hk > _INT:
+        _too_many(where)
     qs, qos = Q.stride(), Qo.stride()
     if d > 1 and not qs[3] == qos[3] == ks_[3] == kos[3] == 1:
         _refuse(where, "a row's elements are contiguous")
@@ -513,6 +522,8 @@ class PagedParams:
 
     def __init__(self, *, B, H, Hkv, page_size, num_pages, max_pages, d=64, dtype="bf16", layout="heads_first",
                  strides=None):
+        if max(B, H, Hkv, d, page_size, num_pages, max_pages) > _INT:
+            _too_many("PagedParams")
         if dtype not in ("bf16", "f32", "f16") or layout not in ("heads_first", "tokens_first"):
             _refuse("PagedParams", "dtype or layout unknown")
         if strides is None:
@@ -569,6 +580,8 @@ def _pools(p, where, Kp, Vp):
 
 def _ints(where, n, *tensors):
     int32 = (_torch or _types()).int32
+    if n > _INT:
+        _too_many(where)
     for t in tensors:
         if t.dtype is not int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
             _refuse(where, "a list is contiguous int32 of the length that goes with the others")
@@ -596,6 +609,8 @@ def paged_append(params, K_new, V_new, Kp, Vp, table, lens, ws, cu=None, rotary=
     the keys are rotated on the way and Q [T, H, d] into Qo."""
     where, p, T = "fs_paged_append", params, K_new.shape[0]
     dt, d, kv = p.dt, p.d, (T, p.Hkv, p.d)
+    if T > _INT:
+        _too_many(where)
     ks, vs = K_new.stride(), V_new.stride()
     if not (K_new.shape == V_new.shape == kv and Kp.shape == Vp.shape == p.shape and
             K_new.dtype is dt and V_new.dtype is dt and Kp.dtype is dt and Vp.dtype is dt and
@@ -647,7 +662,7 @@ def paged_attend(params, Q, Kp, Vp, table, lens, O, ws, lse=None, window=-1, sca
         if lse.get_device() != dev:
             _refuse(where, "all tensors are on one device")
     _call(load().fs_paged_attend, where, dev, stream, p.c, Q.data_ptr(), qs[0], Kp.data_ptr(), Vp.data_ptr(),
-          table.data_ptr(), lens.data_ptr(), int(window), p.scale if scale is None else scale, O.data_ptr(), os_[0],
+          table.data_ptr(), lens.data_ptr(), int(window) if -1 <= window <= _INT else -1 if window < 0 else _INT, p.scale if scale is None else scale, O.data_ptr(), os_[0],
           _ptr(lse), ws.data_ptr(), ws.nbytes)
 
 
