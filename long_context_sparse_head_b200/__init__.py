@@ -661,8 +661,10 @@ def paged_attend(params, Q, Kp, Vp, table, lens, O, ws, lse=None, window=-1, sca
             _refuse(where, "lse is contiguous float32 [B, H]")
         if lse.get_device() != dev:
             _refuse(where, "all tensors are on one device")
+    if not -1 <= window <= _INT:
+        window = -1 if window < 0 else _INT
     _call(load().fs_paged_attend, where, dev, stream, p.c, Q.data_ptr(), qs[0], Kp.data_ptr(), Vp.data_ptr(),
-          table.data_ptr(), lens.data_ptr(), int(window) if -1 <= window <= _INT else -1 if window < 0 else _INT, p.scale if scale is None else scale, O.data_ptr(), os_[0],
+          table.data_ptr(), lens.data_ptr(), int(window), p.scale if scale is None else scale, O.data_ptr(), os_[0],
           _ptr(lse), ws.data_ptr(), ws.nbytes)
 
 

@@ -191,7 +191,7 @@ extern "C" fs_status fs_rotary_init(int r, fs_rope_layout layout, double base, f
     if (!out || r < 2 || r % 2) return FS_ERR_INVALID_ARG;
     if (r > FS_ROPE_MAX_R) return FS_ERR_UNSUPPORTED;
     if (layout != FS_ROPE_INTERLEAVED && layout != FS_ROPE_HALF) return FS_ERR_INVALID_ARG;
-    if (!(base >= 1.0) || !std::isfinite(base) || !std::isfinite(mscale)) return FS_ERR_INVALID_ARG;
+    if (!(base >= 1.0) || !std::isfinite(base) || !std::isfinite((float)mscale)) return FS_ERR_INVALID_ARG;
     if (scaling < FS_ROPE_NONE || scaling > FS_ROPE_BY_PARTS) return FS_ERR_INVALID_ARG;
     if (scaling != FS_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return FS_ERR_INVALID_ARG;
     if (scaling == FS_ROPE_NTK && r == 2) return FS_ERR_INVALID_ARG;        // its exponent r / (r - 2)

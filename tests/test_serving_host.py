@@ -38,6 +38,13 @@ def test_rope_refuses_outputs_folded_together(strides):
     assert rope(strides, Hk=4, H=0) == 1       # the second tensor's output alike
 
 
+@pytest.mark.parametrize("mscale", [3.5e38, -1e300])
+def test_rotary_refuses_a_factor_that_float_does_not_hold(mscale):
+    with pytest.raises(fs.FsError) as e:
+        fs.Rotary(64, mscale=mscale)
+    assert e.value.code == 1
+
+
 # ---------------------------------------------------------------- what the binding passes on
 class Seen(Exception):
     pass
