@@ -100,3 +100,108 @@ def test_sizes_past_32_bits_are_refused(passed):
         with pytest.raises(fs.FsError) as e:
             call()
         assert e.value.code == 2, i
+
+
+def bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def wide(*shape):
+    """A tensor of these sizes, its last dimension's elements two apart."""
+    return bf(*shape[:-1], 2 * shape[-1])[..., ::2]
+
+
+def calls():
+    """Every serving call with arguments that it takes: name -> (function, arguments)."""
+    p, K, V, refs, table, lens, ws = cache()
+    rot = fs.Rotary(64)
+    base = dict(Kp=K, Vp=V, table=table, lens=lens, ws=ws)
+    return {
+        "rope": (fs.rope, dict(rotary=rot, Q=bf(2, 4, 8, 64), Qo=bf(2, 4, 8, 64), K=bf(2, 2, 8, 64), Ko=bf(2, 2, 8, 64),
+                               positions=i32(2, 8))),
+        "rope_backward": (fs.rope_backward, dict(rotary=rot, dQo=bf(2, 4, 8, 64), dQ=bf(2, 4, 8, 64), dKo=bf(2, 2, 8, 64),
+                                                 dK=bf(2, 2, 8, 64), positions=i32(8))),
+        "append": (fs.paged_append, dict(params=p, K_new=bf(5, 2, 64), V_new=bf(5, 2, 64), cu=i32(3), rotary=rot,
+                                         Q=bf(5, 4, 64), Qo=bf(5, 4, 64), **base)),
+        "attend": (fs.paged_attend, dict(params=p, Q=bf(2, 4, 64), O=bf(2, 4, 64), lse=torch.zeros(2, 4), **base)),
+        "reserve": (fs.pages_reserve, dict(params=p, n_new=i32(2), refs=refs, table=table, lens=lens, ws=ws)),
+        "copy": (fs.pages_copy, dict(params=p, Kp=K, Vp=V, src=i32(3), dst=i32(3), ws=ws)),
+        "fork": (fs.pages_fork, dict(params=p, refs=refs, src=i32(1), dst=i32(1), **base)),
+        "free": (fs.pages_free, dict(params=p, refs=refs, table=table, lens=lens, rows=i32(2), ws=ws)),
+        "compact": (fs.pages_compact, dict(params=p, Kp=K, Vp=V, refs=refs, table=table, ws=ws, live=i32(1),
+                                           refs_out=i32(8), table_out=i32(2, 4))),
+    }
+
+
+POOL = [bf(7, 2, 16, 64), bf(8, 2, 16, 64).float(), bf(8, 16, 2, 64).transpose(1, 2), wide(8, 2, 16, 64), bf(8, 2, 16, 128)[..., :64]]
+TABLE = [i32(2, 3), i32(3, 4), i32(2, 4).long(), i32(2, 8)[:, :4], i32(4, 2).t()]
+LENS = [i32(3), i32(2).long(), i32(4)[::2]]
+REFS = [i32(7), i32(8).float(), i32(16)[::2]]
+ROWS = [bf(4, 2, 64), bf(5, 2, 64).half(), bf(5, 2, 128)[..., :64], wide(5, 2, 64), bf(2, 5, 64).transpose(0, 1), bf(5, 128)]
+HEADS = [bf(4, 4, 64), bf(5, 4, 64).float(), bf(5, 4, 128)[..., :64], wide(5, 4, 64), bf(4, 5, 64).transpose(0, 1)]
+STEP = [bf(3, 4, 64), bf(2, 2, 64), bf(2, 4, 64).half(), bf(2, 4, 128)[..., :64], wide(2, 4, 64), bf(4, 2, 64).transpose(0, 1)]
+LIST = [i32(3).long(), i32(6)[::2], i32(3, 1), i32(2)]
+TURNED = [bf(2, 4, 8, 32), bf(2, 4, 7, 64), bf(2, 4, 8, 64).float(), wide(2, 4, 8, 64), bf(2, 4, 64)]
+KEYS = [bf(1, 2, 8, 64), bf(2, 2, 7, 64), bf(2, 2, 8, 64).half(), wide(2, 2, 8, 64), bf(2, 8, 64), None]
+POS = [i32(7), i32(1, 8), i32(2, 8).long(), i32(2, 16)[:, ::2], torch.zeros(2, 8)]
+WRONG = {
+    "rope": dict(Q=TURNED, Qo=TURNED, K=KEYS, Ko=KEYS, positions=POS),
+    "rope_backward": dict(dQo=TURNED, dQ=TURNED, dKo=KEYS, dK=KEYS, positions=POS),
+    "append": dict(K_new=ROWS, V_new=ROWS, Kp=POOL, Vp=POOL, table=TABLE, lens=LENS, cu=[i32(2), i32(4), i32(3).long(), i32(6)[::2]],
+                   Q=HEADS + [None], Qo=HEADS + [None]),
+    "attend": dict(Q=STEP, O=STEP, Kp=POOL, Vp=POOL, table=TABLE, lens=LENS,
+                   lse=[torch.zeros(2, 3), torch.zeros(2, 4).double(), torch.zeros(2, 4).half(), torch.zeros(4, 2).t()]),
+    "reserve": dict(n_new=LENS, refs=REFS, table=TABLE, lens=LENS),
+    "copy": dict(Kp=POOL, Vp=POOL, src=LIST, dst=LIST),
+    "fork": dict(Kp=POOL, Vp=POOL, refs=REFS, table=TABLE, lens=LENS, src=[i32(1).long(), i32(2), i32(1, 1)], dst=[i32(1).long(), i32(2), i32(1, 1)]),
+    "free": dict(refs=REFS, table=TABLE, lens=LENS, rows=[i32(2).long(), i32(4)[::2], i32(2, 1)]),
+    "compact": dict(Kp=POOL, Vp=POOL, refs=REFS, table=TABLE, refs_out=REFS, table_out=TABLE, live=[i32(2), i32(1).long()]),
+}
+
+
+@pytest.mark.parametrize("name", list(WRONG))
+def test_the_binding_takes_what_it_documents(passed, name):
+    call, kw = calls()[name]
+    with pytest.raises(Seen):
+        call(**kw)
+
+
+@pytest.mark.parametrize("name,arg,i", [(n, a, i) for n, w in WRONG.items() for a, v in w.items() for i in range(len(v))])
+def test_the_binding_refuses_each_wrong_tensor(passed, name, arg, i):
+    """One argument wrong in its type, sizes or strides, everything else right: refused by the check
+    of that argument, since nothing else is there to refuse it."""
+    call, kw = calls()[name]
+    with pytest.raises(fs.FsError) as e:
+        call(**{**kw, arg: WRONG[name][arg][i]})
+    assert e.value.code == 1
+
+
+@pytest.mark.parametrize("name", list(WRONG))
+def test_the_binding_refuses_tensors_off_the_gpu(monkeypatch, name):
+    """Right in all else."""
+    def call(*args):
+        raise Seen
+
+    monkeypatch.setattr(fs, "_call", call)
+    call, kw = calls()[name]
+    with pytest.raises(fs.FsError) as e:
+        call(**kw)
+    assert e.value.code == 1
+
+
+def test_a_dimension_of_one_may_have_any_stride(passed):
+    p = fs.PagedParams(B=1, H=1, Hkv=1, d=64, page_size=16, num_pages=1, max_pages=4)
+    K, V, refs, table, lens = fs.alloc_pages(p, "cpu")
+    ws = fs.alloc_paged_workspace(p, "cpu")
+    K, V = (x.as_strided((1, 1, 16, 64), (5, 7, 64, 1)) for x in (K, V))
+    q = bf(1, 1, 64).as_strided((1, 1, 64), (3, 9, 1))
+    with pytest.raises(Seen):
+        fs.paged_attend(p, q, K, V, table, lens, q.clone(), ws)
+    with pytest.raises(Seen):
+        fs.paged_append(p, q, q, K, V, table, lens, ws)
+    with pytest.raises(Seen):
+        fs.rope(fs.Rotary(64), q.view(1, 1, 1, 64), bf(1, 1, 1, 64), positions=i32(1, 2)[:, ::2])
