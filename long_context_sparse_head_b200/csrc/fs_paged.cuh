@@ -15,8 +15,8 @@ struct PagedDev {
 
     // token position -> index into the table row, slot within the page.  pos < 2^30, so the
     // product falls short of pos / ps by less than 1/4 + the fraction: at most one too low.
-    __device__ __forceinline__ void locate(int pos, int &idx, int &slot) const {
-        unsigned q = __umulhi((unsigned)pos, magic);
+    __host__ __device__ __forceinline__ void locate(int pos, int &idx, int &slot) const {
+        unsigned q = (unsigned)((unsigned long long)(unsigned)pos * magic >> 32);
         unsigned r = (unsigned)pos - q * (unsigned)ps;
         if (r >= (unsigned)ps) {
             q++;
@@ -25,7 +25,7 @@ struct PagedDev {
         idx = (int)q;
         slot = (int)r;
     }
-    __device__ __forceinline__ int pages_of(int tokens) const {
+    __host__ __device__ __forceinline__ int pages_of(int tokens) const {
         int q, r;
         locate(tokens, q, r);
         return q + (r != 0);

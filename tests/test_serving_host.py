@@ -1,6 +1,8 @@
 """Refusals of the serving operators at the borders of their ranges (no GPU needed): every call
 here is refused before anything is launched."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -205,3 +207,62 @@ def test_a_dimension_of_one_may_have_any_stride(passed):
         fs.paged_append(p, q, q, K, V, table, lens, ws)
     with pytest.raises(Seen):
         fs.rope(fs.Rotary(64), q.view(1, 1, 1, 64), bf(1, 1, 1, 64), positions=i32(1, 2)[:, ::2])
+
+
+# ---------------------------------------------------------------- positions to pages
+LOCATE = r"""
+#include "fs_paged.cuh"
+#include <cstdio>
+#include <cstdlib>
+
+namespace fs { fs_status paged_dev(const fs_paged_params *p, PagedDev *out); }
+
+int main() {
+    const int top = (1 << 30) - 1;
+    long long seen = 0, wrong = 0;
+    auto check = [&](const fs::PagedDev &P, long long pos) {
+        if (pos < 0 || pos > top) return;
+        int idx, slot;
+        P.locate((int)pos, idx, slot);
+        seen++;
+        wrong += idx != pos / P.ps || slot != pos % P.ps || P.pages_of((int)pos) != (pos + P.ps - 1) / P.ps;
+    };
+    auto all = [&](int page) {
+        fs_paged_params p = {};
+        p.B = p.H = p.Hkv = p.num_pages = p.max_pages = 1;
+        p.d = 64;
+        p.page_size = page;
+        p.token_stride = 64;
+        fs::PagedDev P;
+        // the head's 2^30 elements limit a page of one head to 2^24 tokens
+        if (page > 1 << 24) return;
+        if (fs::paged_dev(&p, &P) != FS_OK) exit(2);
+        const long long last = top / page;
+        for (long long k : {0ll, 1ll, 2ll, 3ll, last / 3, last / 2, last - 1, last})
+            for (long long e = -2; e <= 2; e++) check(P, k * page + e), check(P, k * page + page / 2 + e);
+        check(P, top);
+        unsigned x = 12345u + page;
+        for (int i = 0; i < 200; i++) check(P, (x = x * 1664525u + 1013904223u) >> 2);
+    };
+    for (int page = 1; page <= 20000; page++) all(page);
+    for (int bit = 1; bit <= 24; bit++)
+        for (int e = -1; e <= 1; e++) all((1 << bit) + e > 0 ? (1 << bit) + e : 1);
+    printf("%lld %lld\n", seen, wrong);
+    return wrong != 0;
+}
+"""
+
+
+def test_position_to_page(tmp_path):
+    """The kernels' own division by a reciprocal, compiled for the host, at the borders of every page
+    size to 20000 and of the larger powers of two."""
+    from long_context_sparse_head_b200 import build
+    (tmp_path / "locate.cu").write_text(LOCATE)
+    cmd = [build.NVCC] + build.ARCH + build.FLAGS + ["-I", build.CSRC, str(tmp_path / "locate.cu"), fs.LIB_PATH,
+                                                     "-o", str(tmp_path / "locate")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(tmp_path / "locate")], capture_output=True, text=True,
+                       env={**os.environ, "LD_LIBRARY_PATH": os.path.dirname(fs.LIB_PATH)})
+    seen, wrong = (int(x) for x in r.stdout.split())
+    assert r.returncode == 0 and wrong == 0 and seen > 4e6
