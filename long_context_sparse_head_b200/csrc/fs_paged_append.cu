@@ -135,9 +135,11 @@ cudaError_t launch_as(AppendArgs &A, const void *Q, void *Qo, const void *Kn, co
     A.nrot = Unit::rot_units(A.rot.r);
     A.units = Unit::units(A.P.d, A.rot.r);
     const int per = kAppendThreads / A.units;
-    // rows per thread: as many as leave two threads for every one that the GPU holds at once
-    // (148 x 2048), else one each, for latency
-    // (and at most 65535 blocks for the rows of a token: the most heads make 196605 rows)
+    // Rows per thread: the most that leave 2 x 148 x 2048 threads, else one, for latency (and at
+    // most 65535 blocks for the rows of a token: the most heads make 196605 rows).  At 48 registers
+    // an SM holds 1280 threads, so that is three waves or more.  16 + 4 + 4 heads of 128 in bf16:
+    // 16,384 tokens take four (37 us, one a thread 83), 64 tokens one (3.1, four 3.7).  Between the
+    // two the rule is not at its best: 2,048 tokens take one, 13.0 us, where four take 7.1.
     A.hc = 32;
     auto blocks = [&](int hc) { return (A.Htot + hc - 1) / hc; };
     while (A.hc > 1 && (long long)A.T * A.units * blocks(A.hc) < 2ll * 148 * 2048 && blocks(A.hc / 2) <= 65535)

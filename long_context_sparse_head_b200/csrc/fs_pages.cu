@@ -89,7 +89,7 @@ struct Cluster {
     }
 };
 
-// refs of the pages first .. first + 7; pages past the last read as in use
+// refs of the pages first .. first + 3; pages past the last read as in use
 __device__ __forceinline__ void load_refs(const int32_t *refs, int first, int n, int (&r)[kPerThread]) {
     if (first + kPerThread <= n) {
 #pragma unroll

@@ -3,9 +3,10 @@
 // Pair m of a row turns by the angle pos * theta_m.  A float product would be off by ~0.03 rad
 // at position 2^18, so theta_m / 2 pi is held as a 64-bit fraction of a turn: the 64-bit
 // product with the position wraps at whole turns by itself and is off by at most
-// |pos| * 2^-65 turns.  Its upper 32 bits are reduced to an eighth of a turn either way (an
-// exact integer step) before they become a float, so the argument of sincospi carries a
-// relative error of 2^-24 and no more.
+// |pos| * 2^-65 turns.  Its upper 32 bits are kept (less than 2^-32 turns are cut off) and
+// reduced to an eighth of a turn either way, an exact integer step, before they become a float:
+// the argument of sincospi is off by 2^-32 turns and by 2^-24 of itself, which moves a product
+// by less than 2^-29 of the element beside the fp32 roundings.
 #pragma once
 
 #include <cuda_fp16.h>
